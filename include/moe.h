@@ -97,7 +97,8 @@ typedef enum moe_kernel {
   MOE_K_GATE_UP = 3,       /* grouped gate|up GEMM with the SwiGLU epilogue    */
   MOE_K_DOWN = 4,          /* grouped down GEMM (+ fused weighted combine)     */
   MOE_K_COMBINE = 5,       /* unpermute + weighted combine (staged path)       */
-  MOE_K_OTHER = 6,         /* helpers (router weight split, waits)             */
+  MOE_K_OTHER = 6,         /* helpers (router weight split, waits), the 4-bit calls,
+                              the few-token layer                             */
   MOE_K_COUNT = 7
 } moe_kernel;
 
@@ -365,6 +366,78 @@ moe_status moe_layer_forward_fp8(const moe_shape* shape, const void* x,
                                  const moe_weights* weights, const moe_fp8_experts* experts,
                                  float* out, int32_t* topk_ids, float* topk_w, float* gap,
                                  void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * 4-bit weights in groups. A group of `group` (32, 64 or 128) consecutive elements of a matrix
+ * row has one bf16 scale, and each element a code c in 0..15 standing for (c - 8) * scale:
+ *   scale = bf16(amax_group / 7)             (fp32 division, rounded to nearest even)
+ *   code  = clamp(round_half_even(w / scale), -8, 7) + 8      (8 everywhere if scale is 0)
+ * Storage of a matrix [rows][K] (K is any length; the last group of a row may be short):
+ *   q       uint8 [rows][moe_w4_row_bytes(K)]: 64 bytes for each 128 elements. Element
+ *           32 j + 8 t + i of a block (j, t < 4, i < 8) is nibble (i >> 1) + 4 (i & 1) of the
+ *           block's little-endian 32-bit word 4 t + j; elements behind the row's end hold 8.
+ *   scales  bf16 [rows][moe_w4_row_scales(K, group)]: ceil(K / group) rounded up to a multiple
+ *           of 8, the rest zeros.
+ * A matrix of another shape of this form (a bank [E][rows][K]) is E * rows rows.
+ *
+ * moe_w4_row_bytes, moe_w4_row_scales: sizes of one row (0 for a bad K or group; K <= 2^20).
+ * moe_quantize_w4: w bf16 [rows][K] -> q, scales, padding included; the weight pre-pass, run
+ *   once at load time. A group with an infinite or NaN weight gets a NaN scale.
+ * moe_dequantize_w4: q, scales -> w [rows][K] as MOE_F32 (exact) or MOE_BF16 (rounded once), for
+ *   the calls that take whole matrices (batches that moe_layer_forward_few_w4 is not made for).
+ * moe_matvec_w4: y[t, n] = sum_k x[t, k] W[n, k] for T <= 16 rows of x. W is [N][K] in the
+ *   format above; x is MOE_BF16 or MOE_F16 with row stride ldx elements, y is MOE_F32 or x's
+ *   type with row stride ldy (elements between and behind rows are left as they are). x and y
+ *   need only their element's alignment. Weights enter exactly, sums are fp32, and y is rounded
+ *   once. T == 0, N == 0 and rows == 0 are valid and enqueue nothing.
+ * All asynchronous on `stream`, no workspace. Errors: MOE_ERR_INVALID_ARG (a negative size,
+ * another group or type, a stride below its row, a null or misaligned pointer),
+ * MOE_ERR_UNSUPPORTED (T > 16, K > 2^20, more than 2^31 rows), MOE_ERR_CUDA.
+ */
+typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype;
+
+int64_t moe_w4_row_bytes(int64_t K);
+int64_t moe_w4_row_scales(int64_t K, int32_t group);
+moe_status moe_quantize_w4(int64_t rows, int64_t K, int32_t group, const void* w, void* q,
+                           void* scales, void* stream);
+moe_status moe_dequantize_w4(int64_t rows, int64_t K, int32_t group, const void* q,
+                             const void* scales, moe_dtype w_type, void* w, void* stream);
+moe_status moe_matvec_w4(int32_t T, int64_t N, int64_t K, int32_t group, moe_dtype x_type,
+                         const void* x, int64_t ldx, const void* q, const void* scales,
+                         moe_dtype y_type, void* y, int64_t ldy, void* stream);
+
+/*
+ * The layer for a few tokens: moe_layer_forward in one kernel, for T <= 8 and T * H <= 65536
+ * (MOE_ERR_UNSUPPORTED otherwise; moe_layer_forward takes any batch). Same arguments, workspace
+ * and errors as moe_layer_forward; the variant and the fp16 down operands are not used. It
+ * differs in its arithmetic: the router's logits are summed in 64 bits (topk_ids are the exact
+ * choice, equal logits -> lower index), h keeps its 24 bits, and nothing is added atomically,
+ * so equal calls give equal bits. A token's output depends on its own experts alone.
+ * The kernel's blocks wait for one another (a cooperative launch), each wait bounded: if one ran
+ * out, moe_device_status reports MOE_ERR_DEVICE_TIMEOUT and the outputs are unspecified. The
+ * workspace must have been through moe_workspace_init.
+ *
+ * moe_layer_forward_few_w4: the same with the routed experts in 4-bit groups
+ * (weights->w_gate_up and weights->w_down are not read and may be NULL); the shared expert, its
+ * gate and the router stay as they are. moe_w4_experts: q_gate_up, s_gate_up of the bank
+ * [E][2I][H] (rows 0..I-1 gate, I..2I-1 up), q_down, s_down of [E][H][I], all with groups of
+ * `group`; device pointers, 16-byte aligned, caller-owned.
+ */
+typedef struct moe_w4_experts {
+  const void* q_gate_up;
+  const void* s_gate_up;
+  const void* q_down;
+  const void* s_down;
+  int32_t group;
+} moe_w4_experts;
+
+moe_status moe_layer_forward_few(const moe_shape* shape, const void* x, const moe_weights* weights,
+                                 float* out, int32_t* topk_ids, float* topk_w, float* gap, void* ws,
+                                 size_t ws_bytes, void* stream);
+moe_status moe_layer_forward_few_w4(const moe_shape* shape, const void* x,
+                                    const moe_weights* weights, const moe_w4_experts* experts,
+                                    float* out, int32_t* topk_ids, float* topk_w, float* gap,
+                                    void* ws, size_t ws_bytes, void* stream);
 
 /* Grouped-GEMM variant. moe_workspace_set_variant chooses it for the calls made with the
  * workspace `ws` (its address is the key; moe_workspace_init clears the choice, so a new

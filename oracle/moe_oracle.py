@@ -278,6 +278,67 @@ class Fp8Experts:
         return dequantize_fp8_rows(c, s)
 
 
+# --------------------------------------------------------------------------- 4-bit weights
+# Groups of 32, 64 or 128 elements of a row with one bf16 scale: scale = bf16(amax / 7),
+# code = clamp(round_half_even(w / scale), -8, 7) + 8, weight (code - 8) scale.
+
+def f64_to_bf16(v: np.ndarray) -> np.ndarray:
+    """Finite fp64 -> the nearest bf16 (ties to even) as fp64."""
+    v = np.asarray(v, dtype=np.float64)
+    _, ex = np.frexp(v)
+    step = np.ldexp(1.0, np.maximum(ex - 8, -133))
+    return np.rint(v / step) * step
+
+
+def quantize_w4_rows(w_bf16: np.ndarray, group: int):
+    """uint16 bf16 [rows][K] -> (codes 0..15 uint8 [rows][K], scales fp64 [rows][groups])."""
+    w = bf16_to_f64(w_bf16)
+    rows, K = w.shape
+    codes = np.full((rows, K), 8, dtype=np.uint8)
+    scales = np.zeros((rows, -(-K // group)))
+    for g in range(scales.shape[1]):
+        part = w[:, g * group:(g + 1) * group]
+        s = f64_to_bf16(np.abs(part).max(axis=1) / 7.0)
+        scales[:, g] = s
+        ok = s > 0
+        c = np.clip(np.rint(part[ok] / s[ok, None]), -8, 7) + 8
+        codes[ok, g * group:(g + 1) * group] = c.astype(np.uint8)
+    return codes, scales
+
+
+def dequantize_w4_rows(codes: np.ndarray, scales: np.ndarray, group: int) -> np.ndarray:
+    K = codes.shape[1]
+    return (codes.astype(np.float64) - 8.0) * np.repeat(scales, group, axis=1)[:, :K]
+
+
+def pack_w4_rows(codes: np.ndarray) -> np.ndarray:
+    """Codes [rows][K] -> the stored bytes [rows][64 ceil(K / 128)], element by element."""
+    rows, K = codes.shape
+    n = -(-K // 128)
+    full = np.full((rows, 128 * n), 8, dtype=np.uint8)
+    full[:, :K] = codes
+    out = np.zeros((rows, 64 * n), dtype=np.uint8)
+    for e in range(128 * n):
+        b, j, t, i = e // 128, e // 32 % 4, e // 8 % 4, e % 8
+        nibble = (i >> 1) + 4 * (i & 1)
+        out[:, 64 * b + 4 * (4 * t + j) + nibble // 2] |= full[:, e] << (4 * (nibble & 1))
+    return out
+
+
+class W4Experts:
+    """The routed experts in 4-bit groups, dequantised (fp64), ready for ``moe_forward``."""
+
+    def __init__(self, gate_up: Callable[[int], np.ndarray], down: Callable[[int], np.ndarray],
+                 group: int):
+        self._gu, self._dn, self._group = gate_up, down, group
+
+    def gate_up(self, e: int) -> np.ndarray:
+        return dequantize_w4_rows(*quantize_w4_rows(self._gu(e), self._group), self._group)
+
+    def down(self, e: int) -> np.ndarray:
+        return dequantize_w4_rows(*quantize_w4_rows(self._dn(e), self._group), self._group)
+
+
 # --------------------------------------------------------------------------- dispatch
 
 def permute(ids: np.ndarray, E: int):

@@ -36,6 +36,10 @@ MOE_VARIANT_STREAM = 1
 MOE_VARIANT_TC = 2
 MOE_VARIANT_TC2 = 3
 
+MOE_F32 = 0
+MOE_BF16 = 1
+MOE_F16 = 2
+
 KERNELS = ("router_logits", "router_topk", "permute", "gate_up", "down", "combine", "other")
 MOE_K_COUNT = len(KERNELS)
 
@@ -60,6 +64,11 @@ class moe_fp8_experts(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("q_gate_up", "s_gate_up", "q_down", "s_down")]
 
 
+class moe_w4_experts(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q_gate_up", "s_gate_up", "q_down", "s_down")] + [
+        ("group", ctypes.c_int32)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with "
                       "`python sparse_moe_expert_fp32_b200/build.py` (nvcc, sm_100a)")
@@ -69,6 +78,8 @@ _vp, _sz, _i32, _u64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.
 _SP = ctypes.POINTER(moe_shape)
 _WP = ctypes.POINTER(moe_weights)
 _FP = ctypes.POINTER(moe_fp8_experts)
+_QP = ctypes.POINTER(moe_w4_experts)
+_i64 = ctypes.c_int64
 
 _SIGS = {
     "moe_workspace_bytes": ([_SP], _sz),
@@ -85,6 +96,15 @@ _SIGS = {
     "moe_prepare_down_f16": ([_SP, _vp, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
     "moe_layer_forward_fp8": ([_SP, _vp, _WP, _FP, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
                               ctypes.c_int),
+    "moe_layer_forward_few": ([_SP, _vp, _WP, _vp, _vp, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "moe_layer_forward_few_w4": ([_SP, _vp, _WP, _QP, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+                                 ctypes.c_int),
+    "moe_w4_row_bytes": ([_i64], _i64),
+    "moe_w4_row_scales": ([_i64, _i32], _i64),
+    "moe_quantize_w4": ([_i64, _i64, _i32, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "moe_dequantize_w4": ([_i64, _i64, _i32, _vp, _vp, ctypes.c_int, _vp, _vp], ctypes.c_int),
+    "moe_matvec_w4": ([_i32, _i64, _i64, _i32, ctypes.c_int, _vp, _i64, _vp, _vp, ctypes.c_int, _vp,
+                       _i64, _vp], ctypes.c_int),
     "moe_ep_counts": ([_i32, _i32, _vp, _vp, _vp, _vp], ctypes.c_int),
     "moe_gather_rows": ([ctypes.c_int64, _i32, _vp, ctypes.c_int64, _vp, _vp, _vp, _sz, _vp],
                         ctypes.c_int),
@@ -288,6 +308,154 @@ def moe_layer_forward_fp8(shape, x, weights, experts, out, ws, topk_ids=None, to
            "moe_layer_forward_fp8")
 
 
+# The few-token and 4-bit calls check their tensors against the shapes they stand for: a tensor
+# of another type, device, layout or size is refused before anything is enqueued. Addresses
+# (ints) pass unchecked, as everywhere.
+
+def _need(where: str, t, dtype: str, numel: int, optional: bool = False) -> Optional[int]:
+    """Address of a dense device tensor of `dtype` with at least `numel` elements."""
+    if t is None:
+        if optional:
+            return None
+        raise MoeError(MOE_ERR_INVALID_ARG, where)
+    if isinstance(t, int):
+        return t
+    import torch
+
+    if (t.dtype is not getattr(torch, dtype) or not t.is_cuda or t.numel() < numel
+            or t.get_device() != torch.cuda.current_device() or not t.is_contiguous()):
+        raise MoeError(MOE_ERR_INVALID_ARG, where)
+    return t.data_ptr()
+
+
+def _few_args(where, s, x, weights, out, ws, topk_ids, topk_w, gap, routed):
+    """(x, moe_weights, out, topk_ids, topk_w, gap) of a few-token call."""
+    T, H, E = max(s.T, 0), s.H, s.E
+    if not isinstance(weights, moe_weights):
+        w = weights
+        weights = moe_weights(
+            _need(where, w["w_router"], "float32", E * H),
+            _need(where, w.get("router_bias"), "float32", E, True),
+            _need(where, w["w_gate_up"], "bfloat16", E * 2 * s.I * H) if routed else None,
+            _need(where, w["w_down"], "bfloat16", E * H * s.I) if routed else None,
+            _need(where, w["ws_gate_up"], "bfloat16", 2 * s.Is * H),
+            _need(where, w["ws_down"], "bfloat16", H * s.Is),
+            _need(where, w["w_shared_gate"], "bfloat16", H), None, None)
+    return (_need(where, x, "bfloat16", T * H), weights, _need(where, out, "float32", T * H),
+            _need(where, topk_ids, "int32", T * s.k, True),
+            _need(where, topk_w, "float32", T * s.k, True), _need(where, gap, "float32", T, True),
+            _need(where, ws, "uint8", 0))
+
+
+def moe_layer_forward_few(shape, x, weights, out, ws, topk_ids=None, topk_w=None, gap=None,
+                          stream=None):
+    """The whole layer for T <= 8 tokens in one kernel (T * H <= 65536)."""
+    f = "moe_layer_forward_few"
+    x, w, out, topk_ids, topk_w, gap, wp = _few_args(f, shape, x, weights, out, ws, topk_ids,
+                                                     topk_w, gap, True)
+    _check(_lib.moe_layer_forward_few(ctypes.byref(shape), x, ctypes.byref(w), out, topk_ids,
+                                      topk_w, gap, wp, _nbytes(ws), _stream(stream)), f)
+
+
+def moe_layer_forward_few_w4(shape, x, weights, experts, out, ws, topk_ids=None, topk_w=None,
+                             gap=None, stream=None):
+    """moe_layer_forward_few with the routed experts in 4-bit groups: `experts` is a
+    moe_w4_experts or a dict as quantize_w4_experts returns it."""
+    f = "moe_layer_forward_few_w4"
+    s = shape
+    if not isinstance(experts, moe_w4_experts):
+        g, E, H, I = int(experts["group"]), s.E, s.H, s.I
+        experts = moe_w4_experts(
+            _need(f, experts["q_gate_up"], "uint8", E * 2 * I * _lib.moe_w4_row_bytes(H)),
+            _need(f, experts["s_gate_up"], "bfloat16", E * 2 * I * _lib.moe_w4_row_scales(H, g)),
+            _need(f, experts["q_down"], "uint8", E * H * _lib.moe_w4_row_bytes(I)),
+            _need(f, experts["s_down"], "bfloat16", E * H * _lib.moe_w4_row_scales(I, g)), g)
+    x, w, out, topk_ids, topk_w, gap, wp = _few_args(f, s, x, weights, out, ws, topk_ids, topk_w,
+                                                     gap, False)
+    _check(_lib.moe_layer_forward_few_w4(ctypes.byref(s), x, ctypes.byref(w), ctypes.byref(experts),
+                                         out, topk_ids, topk_w, gap, wp, _nbytes(ws),
+                                         _stream(stream)), f)
+
+
+def moe_w4_row_bytes(K: int) -> int:
+    """Bytes of codes of a 4-bit matrix row of K elements."""
+    n = _lib.moe_w4_row_bytes(int(K))
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_w4_row_bytes")
+    return n
+
+
+def moe_w4_row_scales(K: int, group: int) -> int:
+    """Scales of a 4-bit matrix row of K elements, padding included."""
+    n = _lib.moe_w4_row_scales(int(K), int(group))
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "moe_w4_row_scales")
+    return n
+
+
+def _rows(where, t, dtypes):
+    if t.dtype not in dtypes or t.dim() < 1:
+        raise MoeError(MOE_ERR_INVALID_ARG, where)
+    K = t.shape[-1]
+    return (t.numel() // K if K else 0), K
+
+
+def moe_quantize_w4(w, q, s, group, stream=None) -> None:
+    """w bf16 [..., K] -> codes q uint8 [..., row bytes] and scales s bf16 [..., row scales]."""
+    import torch
+
+    f = "moe_quantize_w4"
+    rows, K = _rows(f, w, (torch.bfloat16,))
+    _check(_lib.moe_quantize_w4(
+        rows, K, int(group), _need(f, w, "bfloat16", 0),
+        _need(f, q, "uint8", rows * _lib.moe_w4_row_bytes(K)),
+        _need(f, s, "bfloat16", rows * _lib.moe_w4_row_scales(K, int(group))), _stream(stream)), f)
+
+
+def moe_dequantize_w4(q, s, w, group, stream=None) -> None:
+    """The inverse into w, fp32 or bf16 [..., K]."""
+    import torch
+
+    f = "moe_dequantize_w4"
+    rows, K = _rows(f, w, (torch.float32, torch.bfloat16))
+    bf16 = w.dtype is torch.bfloat16
+    _check(_lib.moe_dequantize_w4(
+        rows, K, int(group), _need(f, q, "uint8", rows * _lib.moe_w4_row_bytes(K)),
+        _need(f, s, "bfloat16", rows * _lib.moe_w4_row_scales(K, int(group))),
+        MOE_BF16 if bf16 else MOE_F32, _need(f, w, "bfloat16" if bf16 else "float32", 0),
+        _stream(stream)), f)
+
+
+def _strided(where, t, dtype):
+    """(address, row stride) of a device matrix whose rows are dense."""
+    import torch
+
+    T, n = t.shape
+    if (t.dtype is not dtype or not t.is_cuda or t.get_device() != torch.cuda.current_device()
+            or (n > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) < n)):
+        raise MoeError(MOE_ERR_INVALID_ARG, where)
+    return t.data_ptr(), max(t.stride(0), n)
+
+
+def moe_matvec_w4(x, q, s, y, group, stream=None) -> None:
+    """y [T, N] = x [T, K] W^T for T <= 16, W [N, K] as moe_quantize_w4 stores it. x is bf16 or
+    fp16, y is fp32 or x's type; the rows of both may have a stride."""
+    import torch
+
+    f = "moe_matvec_w4"
+    if x.dim() != 2 or y.dim() != 2 or x.shape[0] != y.shape[0]:
+        raise MoeError(MOE_ERR_INVALID_ARG, f)
+    (T, K), N = x.shape, y.shape[1]
+    xt = MOE_F16 if x.dtype is torch.float16 else MOE_BF16
+    yt = MOE_F32 if y.dtype is torch.float32 else xt
+    xp, ldx = _strided(f, x, torch.float16 if xt == MOE_F16 else torch.bfloat16)
+    yp, ldy = _strided(f, y, y.dtype if yt == MOE_F32 else x.dtype)
+    _check(_lib.moe_matvec_w4(
+        T, N, K, int(group), xt, xp, ldx, _need(f, q, "uint8", N * _lib.moe_w4_row_bytes(K)),
+        _need(f, s, "bfloat16", N * _lib.moe_w4_row_scales(K, int(group))), yt, yp, ldy,
+        _stream(stream)), f)
+
+
 def _ws_args(ws):
     return (None, 0) if ws is None else (_ptr(ws), _nbytes(ws))
 
@@ -430,3 +598,26 @@ def prepare_down_f16(shape: moe_shape, weights: dict, stream=None) -> dict:
     st, flags = moe_device_status(ws, stream)
     _check(st, "moe_prepare_down_f16 (device)")
     return out
+
+
+def quantize_w4(w, group: int = 32, stream=None):
+    """A bf16 matrix or bank [..., K] in 4-bit groups: (codes uint8, scales bf16), allocated."""
+    import torch
+
+    lead = tuple(w.shape[:-1])
+    q = torch.empty(lead + (moe_w4_row_bytes(w.shape[-1]),), dtype=torch.uint8, device=w.device)
+    s = torch.empty(lead + (moe_w4_row_scales(w.shape[-1], group),), dtype=torch.bfloat16,
+                    device=w.device)
+    moe_quantize_w4(w, q, s, group, stream)
+    return q, s
+
+
+def quantize_w4_experts(shape: moe_shape, weights: dict, group: int = 32, stream=None) -> dict:
+    """The 4-bit expert pre-pass on a weight dict (run once): allocates and returns {q_gate_up,
+    s_gate_up, q_down, s_down, group} on the routed banks' device."""
+    E, H, I = shape.E, shape.H, shape.I
+    gu, dn = weights["w_gate_up"].view(E, 2 * I, H), weights["w_down"].view(E, H, I)
+    q = {"group": int(group)}
+    q["q_gate_up"], q["s_gate_up"] = quantize_w4(gu, group, stream)
+    q["q_down"], q["s_down"] = quantize_w4(dn, group, stream)
+    return q

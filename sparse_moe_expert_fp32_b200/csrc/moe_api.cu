@@ -12,6 +12,7 @@
 
 #include "moe_internal.h"
 #include "tc_gemm.h"
+#include "w4.cuh"
 
 namespace moe {
 
@@ -52,6 +53,8 @@ Layout layout(const moe_shape& s) {
   L.xs = take(std::max(R * H * sizeof(uint16_t), fp8_h_pieces_bytes(s) + R * sizeof(float)));
   L.h_plane = (R + T) * (size_t)L.ldh;
   L.h = take(2 * L.h_plane * sizeof(uint16_t));
+  const size_t few_t = std::min(T, (size_t)kFewMaxT);
+  L.few_h = take(3 * few_t * (k + 1) * (size_t)L.ldh * sizeof(uint16_t));
   L.total = o;
   return L;
 }
@@ -156,6 +159,21 @@ moe_status check_expert_weights(const moe_weights* w) {
     return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
+
+moe_status check_layer_io(const void* x, const float* out, const int32_t* topk_ids,
+                          const float* topk_w, const float* gap) {
+  if (!aligned16(x) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+  if ((topk_ids && !aligned16(topk_ids)) || (topk_w && !aligned16(topk_w)) || (gap && !aligned16(gap)))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// log2(group / 32) of a 4-bit weight group, -1 for a size the format does not have
+int w4_shift(int32_t group) { return group == 32 ? 0 : group == 64 ? 1 : group == 128 ? 2 : -1; }
+
+constexpr int64_t kW4MaxK = (int64_t)1 << 20;     // row length
+constexpr int64_t kW4MaxRows = (int64_t)1 << 31;  // rows of a matrix, or of a bank of them
+constexpr int32_t kW4MaxT = 16;
 
 moe_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
@@ -524,6 +542,96 @@ moe_status moe_layer_forward_fp8(const moe_shape* shape, const void* x, const mo
                           st));
   MOE_CUDA(launch_tc8_gate_up(s, L, w, xb, sorted_token, *weights, *experts, st));
   MOE_CUDA(launch_tc8_down(s, L, w, sorted_token, sorted_w, sg, *weights, *experts, out, st));
+  return MOE_OK;
+}
+
+moe_status moe_layer_forward_few(const moe_shape* shape, const void* x, const moe_weights* weights,
+                                 float* out, int32_t* topk_ids, float* topk_w, float* gap, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  MOE_TRY(check_shape(shape));
+  const moe_shape& s = *shape;
+  MOE_TRY(check_router_weights(weights));
+  MOE_TRY(check_expert_weights(weights));
+  MOE_TRY(check_layer_io(x, out, topk_ids, topk_w, gap));
+  if (!few_supported(s)) return MOE_ERR_UNSUPPORTED;
+  MOE_TRY(check_ws(s, ws, ws_bytes));
+  if (s.T == 0) return MOE_OK;
+  MOE_CUDA(launch_few_layer(s, layout(s), static_cast<char*>(ws), static_cast<const uint16_t*>(x),
+                            *weights, nullptr, out, topk_ids, topk_w, gap, sm_count_host(),
+                            (cudaStream_t)stream));
+  return MOE_OK;
+}
+
+moe_status moe_layer_forward_few_w4(const moe_shape* shape, const void* x,
+                                    const moe_weights* weights, const moe_w4_experts* experts,
+                                    float* out, int32_t* topk_ids, float* topk_w, float* gap,
+                                    void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(check_shape(shape));
+  const moe_shape& s = *shape;
+  MOE_TRY(check_router_weights(weights));
+  if (!aligned16(weights->ws_gate_up) || !aligned16(weights->ws_down)) return MOE_ERR_INVALID_ARG;
+  if (!experts || !aligned16(experts->q_gate_up) || !aligned16(experts->s_gate_up) ||
+      !aligned16(experts->q_down) || !aligned16(experts->s_down) ||
+      w4_shift(experts->group) < 0)
+    return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_layer_io(x, out, topk_ids, topk_w, gap));
+  if (!few_supported(s)) return MOE_ERR_UNSUPPORTED;
+  MOE_TRY(check_ws(s, ws, ws_bytes));
+  if (s.T == 0) return MOE_OK;
+  MOE_CUDA(launch_few_layer(s, layout(s), static_cast<char*>(ws), static_cast<const uint16_t*>(x),
+                            *weights, experts, out, topk_ids, topk_w, gap, sm_count_host(),
+                            (cudaStream_t)stream));
+  return MOE_OK;
+}
+
+int64_t moe_w4_row_bytes(int64_t K) { return K < 1 || K > kW4MaxK ? 0 : w4_row_bytes(K); }
+
+int64_t moe_w4_row_scales(int64_t K, int32_t group) {
+  return K < 1 || K > kW4MaxK || w4_shift(group) < 0 ? 0 : w4_row_scales(K, group);
+}
+
+moe_status moe_quantize_w4(int64_t rows, int64_t K, int32_t group, const void* w, void* q,
+                           void* scales, void* stream) {
+  const int shift = w4_shift(group);
+  if (rows < 0 || K < 1 || shift < 0) return MOE_ERR_INVALID_ARG;
+  if (K > kW4MaxK || rows > kW4MaxRows) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!aligned16(w) || !aligned16(q) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+  MOE_CUDA(launch_quantize_w4(static_cast<const uint16_t*>(w), rows, K, shift,
+                              static_cast<uint8_t*>(q), static_cast<uint16_t*>(scales),
+                              sm_count_host(), (cudaStream_t)stream));
+  return MOE_OK;
+}
+
+moe_status moe_dequantize_w4(int64_t rows, int64_t K, int32_t group, const void* q,
+                             const void* scales, moe_dtype w_type, void* w, void* stream) {
+  const int shift = w4_shift(group);
+  if (rows < 0 || K < 1 || shift < 0 || (w_type != MOE_F32 && w_type != MOE_BF16))
+    return MOE_ERR_INVALID_ARG;
+  if (K > kW4MaxK || rows > kW4MaxRows) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!aligned16(w) || !aligned16(q) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+  MOE_CUDA(launch_dequantize_w4(static_cast<const uint8_t*>(q), static_cast<const uint16_t*>(scales),
+                                rows, K, shift, w, w_type == MOE_BF16, sm_count_host(),
+                                (cudaStream_t)stream));
+  return MOE_OK;
+}
+
+moe_status moe_matvec_w4(int32_t T, int64_t N, int64_t K, int32_t group, moe_dtype x_type,
+                         const void* x, int64_t ldx, const void* q, const void* scales,
+                         moe_dtype y_type, void* y, int64_t ldy, void* stream) {
+  const int shift = w4_shift(group);
+  if (T < 0 || N < 0 || K < 1 || shift < 0) return MOE_ERR_INVALID_ARG;
+  if ((x_type != MOE_BF16 && x_type != MOE_F16) || (y_type != MOE_F32 && y_type != x_type))
+    return MOE_ERR_INVALID_ARG;
+  if (T > kW4MaxT || K > kW4MaxK || N > kW4MaxRows) return MOE_ERR_UNSUPPORTED;
+  if (T == 0 || N == 0) return MOE_OK;
+  if (!x || ((uintptr_t)x & 1u) || !y || ((uintptr_t)y & (y_type == MOE_F32 ? 3u : 1u)) ||
+      (T > 1 && (ldx < K || ldy < N)) || !aligned16(q) || !aligned16(scales))
+    return MOE_ERR_INVALID_ARG;
+  MOE_CUDA(launch_matvec_w4(T, N, K, shift, static_cast<const uint16_t*>(x), x_type == MOE_F16, ldx,
+                            static_cast<const uint8_t*>(q), static_cast<const uint16_t*>(scales), y,
+                            y_type == MOE_F32, ldy, sm_count_host(), (cudaStream_t)stream));
   return MOE_OK;
 }
 

@@ -14,6 +14,12 @@ constexpr int kMaxE = 1024;
 constexpr int kMaxK = 32;
 constexpr int kPermBlock = 256;  // tokens per dispatch block (one bit per token in a mask)
 constexpr int kTcChunk = 256;    // max tokens (MMA N) per tensor-core tile
+// Few-token layer: tokens in one MMA's columns; x stays in shared memory.
+constexpr int kFewMaxT = 8;
+constexpr int64_t kFewMaxTH = 65536;
+// Words kFewSyncWord .. + 2 of the status region count its grid barriers: zero from
+// moe_workspace_init on, and left zero by every call.
+constexpr int kFewSyncWord = 16;
 constexpr uint32_t kFlagBounds = 1u;
 constexpr uint32_t kFlagTimeout = 2u;
 constexpr uint32_t kFlagRange = 4u;  // a value saturated to fit fp16 (down operands)
@@ -43,6 +49,8 @@ struct Layout {
   size_t h;             // bf16 [2][T*k + T][ldh]: SwiGLU intermediate as a hi|lo pair of planes
                         // (h = hi + lo), routed rows then shared rows
   size_t h_plane;       // elements per plane: (T*k + T) * ldh
+  size_t few_h;         // bf16 [3][pairs][ldh]: h of the few-token layer in three pieces, pairs =
+                        // (k+1) * min(T, kFewMaxT); its logits are doubles in `logits`
   size_t total;
   int nblk;
   int ldh;              // max(I, Is)
@@ -174,6 +182,19 @@ cudaError_t launch_quantize_fp8_rows(const uint16_t* w, size_t rows, int n, uint
 // Down-projection weights re-encoded as fp16(W * 2^8) (down_f16.cu); n a multiple of 8.
 cudaError_t launch_down_to_f16(const uint16_t* w, size_t n, uint16_t* out, uint32_t* status,
                                int sms, cudaStream_t st);
+// 4-bit weights (w4_quant.cu, w4_matvec.cu); groups of 32 << shift elements.
+cudaError_t launch_quantize_w4(const uint16_t* w, int64_t rows, int64_t K, int shift, uint8_t* q,
+                               uint16_t* scales, int sms, cudaStream_t st);
+cudaError_t launch_dequantize_w4(const uint8_t* q, const uint16_t* scales, int64_t rows, int64_t K,
+                                 int shift, void* out, bool bf16, int sms, cudaStream_t st);
+cudaError_t launch_matvec_w4(int T, int64_t N, int64_t K, int shift, const uint16_t* x, bool f16,
+                             int64_t ldx, const uint8_t* q, const uint16_t* s, void* y, bool y_f32,
+                             int64_t ldy, int sms, cudaStream_t st);
+// The layer for a few tokens in one kernel (few_layer.cu); q = NULL: bf16 experts.
+bool few_supported(const moe_shape& s);
+cudaError_t launch_few_layer(const moe_shape& s, const Layout& L, char* ws, const uint16_t* x,
+                             const moe_weights& w, const moe_w4_experts* q, float* out,
+                             int32_t* ids, float* topk_w, float* gap, int sms, cudaStream_t st);
 cudaError_t launch_wait_flag(const int32_t* flag, uint64_t timeout_ns, uint32_t* status,
                              cudaStream_t st);
 
