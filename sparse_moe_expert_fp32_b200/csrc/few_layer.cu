@@ -23,168 +23,367 @@
 // NaN weight stays within the tokens that chose its expert).
 #include <float.h>
 
-#include <mutex>
+#include <algorithm>
 
 #include "moe_internal.h"
+#include "sm100_ptx.cuh"
+#include "tc_common.cuh"
 #include "w4.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kFewWarps = 16;
+constexpr int kFewWarps = 8;     // consumers
 constexpr int kFewThreads = kFewWarps * 32;
+constexpr int kFewTeam = 4;      // warps that share a stage; the stages go to the teams in turn
+constexpr int kFewTeams = kFewWarps / kFewTeam;
+constexpr int kFewBlock = kFewThreads + 2 * 32;  // and one warp that feeds them weights, one h
 constexpr int kFewPairs = kFewMaxT * (kMaxK + 1);  // (token, expert) pairs, shared expert included
 constexpr int kFewRows = 32;                       // output rows of one pass of the down stage
-static_assert(2 * 16 * kFewMaxT == kFewRows * kFewMaxT, "the two users of FewShared::red");
+constexpr int kFewMaxStages = 8;
+constexpr int kFewMinStage = 15360;  // holds 28 rows of eight blocks with scales, 32 rows of five (few_chunks)
 constexpr uint64_t kFewWaitNs = 2000000000ull;
+constexpr uint64_t kFewDrainNs = 200000000ull;
+constexpr int kBarConsumers = 1, kBarRouted = 2;   // named barriers
+
+// How a weight matrix comes through the ring: `n` chunks of a row, `cb` 64-byte blocks each (a block
+// is 32 bf16 or 128 4-bit weights); scales `sc` bytes of a row and chunk.
+struct FewChunks {
+  int n, cb, sc, blocks;
+};
 
 struct FewArgs {
   const uint16_t* x;
   const float* w_router;
   const float* bias;
   const uint16_t* wsg;
-  const uint8_t* gate_up;  // routed banks: bf16, or codes
-  const uint8_t* down;
-  const uint16_t* s_gate_up;  // scales of the codes
-  const uint16_t* s_down;
-  const uint16_t* ws_gate_up;
-  const uint16_t* ws_down;
   float* out;
   int32_t* ids;
   float* w;
   float* gap;
-  double* logits;   // [T][E]
-  uint16_t* h;      // [3][pairs][ldh]
-  size_t h_plane;
+  double* logits;   // [T][ldl]: router logits, then the shared expert's gate; rows of 16-byte units
+  uint16_t* h;      // [pairs][ldh / 32][3][32]: three pieces of 32 channels side by side
   uint32_t* sync;   // barrier counters: zero between calls
   uint32_t* status;
-  int T, H, E, k, I, Is, ldh, shift;
+  int T, H, E, k, I, Is, ldh, ldl, shift;
+  FewChunks gu, gu_s, dn, dn_s;  // gate|up and down matrices, routed and shared
+  int rows;                      // output rows of a pass
+  int stages, stage_bytes;
+  int unit, units, h_bytes;      // ring of h: bytes of a token's chunk, number of them, region
+};
+
+// Tensor maps of the weights (bytes; innermost first), each stage one box of each:
+//   gate|up  [64][channel][block][gate, up][expert], box 64 x 8 x cb x 2 x 1
+//   down     [64][output row][block][expert], box 64 x rows x cb x 1
+//   scales   [bytes of a row][channel][gate, up][expert] and [bytes of a row][output row][expert]
+struct FewMaps {
+  CUtensorMap gu, gu_s, dn, dn_s, gu_sc, dn_sc;
 };
 
 struct FewShared {
-  double part[kFewWarps][32];               // router partial sums
-  float red[2][kFewWarps][16 * kFewMaxT];   // cross-warp sums; the down stage uses both halves
+  uint64_t full[kFewMaxStages], empty[kFewMaxStages], x_full, logits_full;
+  uint8_t stage_units[kFewMaxStages];       // units of h that a stage in flight uses
+  union {
+    double part[2 * kFewWarps * 16 * kFewMaxT / 2];  // router partial sums: [stage][warp of the team][token]
+    struct {
+      uint64_t key[kFewMaxT][64];            // selection: candidates of a token
+      uint16_t e[kFewMaxT][64];
+    } cand;
+    float red[2][kFewWarps][16 * kFewMaxT];  // cross-warp sums; the down stage uses both halves
+  };
   uint32_t mask[kMaxE];                     // tokens that chose an expert
   uint16_t index[kMaxE];                    // its place among the active ones
-  int scan[2 * kFewWarps + 2];
+  int scan[kFewWarps];
+  double sel_v[kFewMaxT][kMaxK + 1];
   float sel_w[kFewMaxT][kMaxK];
-  int16_t sel_e[kFewMaxT][kMaxK];
-  float sgate[kFewMaxT];
+  int16_t sel_e[kFewMaxT][kMaxK + 1];
+  float sgate[kFewMaxT];                    // zero behind the last token
   float pair_w[kFewPairs];
   int16_t act_e[kFewMaxT * kMaxK + 1];      // entry 0: the shared expert
   int16_t act_pair[kFewMaxT * kMaxK + 1];   // first pair of the expert
   uint8_t act_mask[kFewMaxT * kMaxK + 1];
   int n_act;
+  int aborted;
 };
+static_assert(2 * 16 * kFewMaxT == kFewRows * kFewMaxT, "the two users of FewShared::red");
 
-__device__ __forceinline__ uint4 ld_cg_v4(const void* p) {
-  return __ldcg(reinterpret_cast<const uint4*>(p));
+constexpr size_t kFewSharedBytes = (sizeof(FewShared) + 127) / 128 * 128;
+constexpr size_t kFewSmem = 227 * 1024;
+
+__device__ __forceinline__ void sync_consumers() { ptx::bar_sync(kBarConsumers, kFewThreads); }
+
+__device__ __forceinline__ void give_up(FewShared& S, uint32_t* status) {
+  *reinterpret_cast<volatile int*>(&S.aborted) = 1;
+  set_flag(status, kFlagTimeout);
 }
 
+// Bounded wait on an mbarrier phase; false once any wait of the block has run out.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, FewShared& S, uint32_t* status) {
+  uint64_t t0 = 0;
+  for (uint32_t spin = 1;; ++spin) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if ((spin & 31u) == 0) {  // reading the clock is slow: only in long waits
+      if (*reinterpret_cast<volatile int*>(&S.aborted)) return false;
+      const uint64_t t = globaltimer_ns();
+      if (!t0) t0 = t;
+      if (t - t0 > kFewWaitNs) {
+        give_up(S, status);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, FewShared& S, uint32_t* status) {
+  if (ptx::mbar_test_wait(bar, parity)) return true;
+  return wait_slow(bar, parity, S, status);
+}
+
+// Grid barriers. Bounded: on expiry the flag is set and the kernel runs on with what it has
+// (nothing it reads then is used as an address).
 __device__ __forceinline__ void grid_arrive(uint32_t* c) {
-  __syncthreads();
+  sync_consumers();
   if (threadIdx.x == 0) {
     __threadfence();
     atomicAdd(c, 1u);
   }
 }
-
-// Bounded: on expiry the flag is set and the kernel runs on with what it has.
-__device__ __forceinline__ void grid_wait(uint32_t* c, uint32_t* status) {
-  if (threadIdx.x == 0) {
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t spin = 1;; ++spin) {
-      uint32_t v;
-      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(c) : "memory");
-      if (v >= gridDim.x) break;
-      if ((spin & 63u) == 0 && globaltimer_ns() - t0 > kFewWaitNs) {
-        set_flag(status, kFlagTimeout);
+__device__ __forceinline__ void grid_wait(uint32_t* c, FewShared& S, uint32_t* status) {
+  uint64_t t0 = 0;
+  for (uint32_t spin = 1;; ++spin) {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(c) : "memory");
+    if (v >= gridDim.x) break;
+    if ((spin & 63u) == 0) {
+      const uint64_t t = globaltimer_ns();
+      if (!t0) t0 = t;
+      if (t - t0 > kFewWaitNs) {
+        give_up(S, status);
         break;
       }
     }
-    __threadfence();
   }
-  __syncthreads();
+  __threadfence();
 }
 
-// Order-preserving key of a logit: larger key = larger value, NaN below everything, 0 = none.
+// ---------------------------------------------------------------- the ring
+// Weights reach the consumers through a ring of stages in shared memory, filled by TMA: the copies
+// in flight hold no registers, and the feeding thread runs ahead of the consumers across their
+// barriers, so that HBM works on the down matrices while the last gate|up tiles are summed and the
+// grid waits for h. A stage is a K chunk of some weight rows, [block][row][64 bytes]: one box, so
+// one instruction (row by row copies of 1.3 KB are issue bound at 5.0 TB/s, boxes reach 6.9), and a
+// warp reads 8 rows of a block as 512 bytes in a row. In the down stage h of the expert's tokens
+// comes through a second ring, a unit a token and chunk, in the place where x was.
+struct Cursor {
+  int s;
+  uint32_t parity;
+  __device__ void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// A consumer's place: the number of the stage its team takes next, and the ring's slot for it.
+struct Place {
+  int i;
+  Cursor cur;
+  __device__ void next(int stages) {
+    i += kFewTeams;
+    cur.s += kFewTeams;
+    while (cur.s >= stages) {
+      cur.s -= stages;
+      cur.parity ^= 1u;
+    }
+  }
+};
+
+__device__ __forceinline__ int round128(int v) { return (v + 127) & ~127; }
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          ptx::smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(ptx::smem_u32(bar))
+      : "memory");
+}
+
+#define MOE_TMA_LOAD(N) \
+  "cp.async.bulk.tensor." N "d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+__device__ __forceinline__ void tma_3d(void* dst, const void* map, uint64_t* bar, int c0, int c1, int c2) {
+  asm volatile(MOE_TMA_LOAD("3") "{%3, %4, %5}], [%2];" ::"r"(ptx::smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+__device__ __forceinline__ void tma_4d(void* dst, const void* map, uint64_t* bar, int c0, int c1, int c2, int c3) {
+  asm volatile(MOE_TMA_LOAD("4") "{%3, %4, %5, %6}], [%2];" ::"r"(ptx::smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
+__device__ __forceinline__ void tma_5d(void* dst, const void* map, uint64_t* bar, int c0, int c1, int c2, int c3,
+                                       int c4) {
+  asm volatile(MOE_TMA_LOAD("5") "{%3, %4, %5, %6, %7}], [%2];" ::"r"(ptx::smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+               "r"(c4)
+               : "memory");
+}
+
+// A thread that follows the stages in the consumers' order and does its part of each.
+struct Feeder {
+  const FewArgs& a;
+  FewShared& S;
+  uint8_t* ring;
+  Cursor cur;
+  int issued;  // stages filled so far, up to the ring's size
+  bool ok;
+
+  __device__ uint8_t* begin() {
+    ok = ok && wait_phase(&S.empty[cur.s], cur.parity ^ 1u, S, a.status);
+    return ring + (size_t)cur.s * a.stage_bytes;
+  }
+  __device__ void end() {
+    cur.next(a.stages);
+    if (issued < a.stages) ++issued;
+  }
+  // leave no copy in flight: wait for the last phase of every stage that was filled
+  __device__ void drain() {
+    for (int i = 0; i < issued; ++i) {
+      cur.s = cur.s ? cur.s - 1 : a.stages - 1;
+      if (cur.s == a.stages - 1) cur.parity ^= 1u;
+      uint64_t t0 = 0;
+      while (!ptx::mbar_try_wait(&S.full[cur.s], cur.parity)) {
+        const uint64_t t = globaltimer_ns();
+        if (!t0) t0 = t;
+        if (t - t0 > kFewDrainNs) break;
+      }
+    }
+  }
+};
+
+// Order-preserving keys of a logit: larger key = larger value, NaN below everything but 0, which is
+// none. (-0 does not occur: the sums start from +0.) high_key: from its upper half, with the lowest
+// bit set, so that values with equal upper halves have equal keys.
 __device__ __forceinline__ uint64_t logit_key(double v) {
-  const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);  // -0 and +0 are equal
-  const uint64_t k = (b >> 63) ? ~b : (b | 0x8000000000000000ull);
-  return v == v ? k : 1ull;
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  return v == v ? b ^ (b >> 63 ? ~0ull : 1ull << 63) : 1ull;
 }
-__device__ __forceinline__ double key_logit(uint64_t k) {
-  if (k == 1ull) return __longlong_as_double(0x7ff8000000000000ll);
-  return __longlong_as_double((long long)((k >> 63) ? (k & 0x7fffffffffffffffull) : ~k));
+__device__ __forceinline__ uint32_t high_key(int high) {
+  if ((high & 0x7fffffff) > 0x7ff00000) return 1u;
+  return ((uint32_t)(high ^ ((high >> 31) | (int)0x80000000)) | 1u);
 }
 
-// One warp: top-k of token t (largest first, ties to the lowest index), softmax over the chosen.
-__device__ void select_token(const FewArgs& a, FewShared& S, int t, int lane) {
-  constexpr int VPL = kMaxE / 32;
-  uint64_t key[VPL];
+// Top-k of token t by one warp (largest first, ties to the lowest index), softmax over the chosen;
+// `row` holds its logits in shared memory, VPL a lane. The (k+1)-th largest of the lanes' maxima (of
+// the keys' upper halves) bounds the (k+1)-th largest logit from below, so only those at or above it
+// (about 1.5 k) are ranked, two a lane, each against all others. If more than 64 are left (k close to
+// 32, many equal logits), k + 1 rounds of a warp maximum take their place. One warp, nothing to hide
+// its latencies behind: the loops are unrolled for independent instructions.
+template <int VPL>
+__device__ __forceinline__ void select_token(const FewArgs& a, FewShared& S, const double* row, int t, int lane) {
+  constexpr uint32_t all = 0xffffffffu;
+  const int* half = reinterpret_cast<const int*>(row) + 1;
+  const int rounds = a.k < a.E ? a.k + 1 : a.k;
+  uint32_t high[VPL], best = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const int e = lane + 32 * i;
-    key[i] = 0;
-    if (e < a.E) {
-      double v = __ldcg(a.logits + (size_t)t * a.E + e);
-      if (a.bias) v += (double)__ldg(a.bias + e);
-      key[i] = logit_key(v);
+    const uint32_t key = high_key(half[2 * min(lane + 32 * i, a.E - 1)]);
+    high[i] = lane + 32 * i < a.E ? key : 0u;
+    best = max(best, high[i]);
+  }
+  uint32_t bound = 1;  // every expert's key is at least 1
+  if (VPL > 2 && rounds <= 32) {
+    int rank = 0;
+#pragma unroll
+    for (int o = 0; o < 32; ++o) {
+      const uint32_t other = __shfl_sync(all, best, o);
+      rank += other > best || (other == best && o < lane);
+    }
+    bound = max(__shfl_sync(all, best, __ffs(__ballot_sync(all, rank == rounds - 1)) - 1), 1u);
+  }
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const uint32_t m = __ballot_sync(all, high[i] >= bound);
+    const int at = n + __popc(m & ((1u << lane) - 1u));
+    if (high[i] >= bound && at < 64) S.cand.e[t][at] = (uint16_t)(lane + 32 * i);
+    n += __popc(m);
+  }
+  __syncwarp();
+  if (n <= 64) {
+    // candidates are in ascending order of the expert: ties go to the lower place
+    const int e0 = S.cand.e[t][min(lane, n - 1)], e1 = S.cand.e[t][min(lane + 32, n - 1)];
+    const uint64_t k0 = lane < n ? logit_key(row[e0]) : 0ull, k1 = lane + 32 < n ? logit_key(row[e1]) : 0ull;
+    S.cand.key[t][lane] = k0;
+    S.cand.key[t][lane + 32] = k1;
+    __syncwarp();
+    int r0 = 0, r1 = 0;
+    for (int i0 = 0; i0 < n; i0 += 8)
+#pragma unroll
+      for (int i = i0; i < i0 + 8; ++i) {
+        const uint64_t other = S.cand.key[t][i];
+        r0 += other > k0 || (other == k0 && i < lane);
+        r1 += other > k1 || (other == k1 && i < lane + 32);
+      }
+    if (lane < n && r0 < rounds) {
+      S.sel_v[t][r0] = row[e0];
+      S.sel_e[t][r0] = (int16_t)e0;
+    }
+    if (lane + 32 < n && r1 < rounds) {
+      S.sel_v[t][r1] = row[e1];
+      S.sel_e[t][r1] = (int16_t)e1;
+    }
+  } else {
+    uint32_t taken = 0;
+    for (int r = 0; r < rounds; ++r) {
+      uint64_t top = 0;
+      int be = 0x7fffffff;
+      for (int e = lane, i = 0; e < a.E; e += 32, ++i) {
+        const uint64_t key = logit_key(row[e]);
+        if (!((taken >> i) & 1u) && key > top) {
+          top = key;
+          be = e;
+        }
+      }
+      const uint32_t hi = __reduce_max_sync(all, (uint32_t)(top >> 32));
+      bool c = (uint32_t)(top >> 32) == hi;
+      const uint32_t lo = __reduce_max_sync(all, c ? (uint32_t)top : 0u);
+      c = c && (uint32_t)top == lo;
+      const int e = __reduce_min_sync(all, c ? be : 0x7fffffff);
+      if (lane == 0) {
+        S.sel_v[t][r] = row[e];
+        S.sel_e[t][r] = (int16_t)e;
+      }
+      if ((e & 31) == lane) taken |= 1u << (e >> 5);
     }
   }
-  int my_e = 0;
-  double my_v = 0.0, next = 0.0;
-  const int rounds = a.k < a.E ? a.k + 1 : a.k;
-  for (int r = 0; r < rounds; ++r) {
-    uint64_t best = 0;
-    int be = 0x7fffffff;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        be = lane + 32 * i;
-      }
-    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(best >> 32));
-    bool c = (uint32_t)(best >> 32) == hi;
-    const uint32_t lo = __reduce_max_sync(0xffffffffu, c ? (uint32_t)best : 0u);
-    c = c && (uint32_t)best == lo;
-    const int e = __reduce_min_sync(0xffffffffu, c ? be : 0x7fffffff);
-    const double v = key_logit(((uint64_t)hi << 32) | lo);
-    if (r < a.k) {
-      if (lane == r) {
-        my_e = e;
-        my_v = v;
-      }
-    } else {
-      next = v;
-    }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (e == lane + 32 * i) key[i] = 0;
-  }
-  const double vmax = __shfl_sync(0xffffffffu, my_v, 0);
-  const float ex = lane < a.k ? expf((float)(my_v - vmax)) : 0.f;
+  __syncwarp();
+  const int e = S.sel_e[t][min(lane, a.k - 1)];
+  const float ex = lane < a.k ? expf((float)(S.sel_v[t][min(lane, a.k - 1)] - S.sel_v[t][0])) : 0.f;
   const float p = ex / warp_sum(ex);
   if (lane < a.k) {
-    S.sel_e[t][lane] = (int16_t)my_e;
     S.sel_w[t][lane] = p;
-    atomicOr(&S.mask[my_e], 1u << t);
+    atomicOr(&S.mask[e], 1u << t);
     if (blockIdx.x == 0) {
-      if (a.ids) a.ids[(size_t)t * a.k + lane] = my_e;
+      if (a.ids) a.ids[(size_t)t * a.k + lane] = e;
       if (a.w) a.w[(size_t)t * a.k + lane] = p;
     }
   }
-  const double kth = __shfl_sync(0xffffffffu, my_v, a.k - 1);
   if (blockIdx.x == 0 && a.gap && lane == 0)
-    a.gap[t] = a.k < a.E ? (float)(kth - next) : __int_as_float(0x7f800000);
+    a.gap[t] = a.k < a.E ? (float)(S.sel_v[t][a.k - 1] - S.sel_v[t][a.k]) : __int_as_float(0x7f800000);
 }
 
-// The active experts in ascending order, and the pairs (expert, token) in that order.
+// The active experts in ascending order, and the pairs (expert, token) in that order. The feeders
+// start as soon as they know the experts.
 __device__ void build_active(const FewArgs& a, FewShared& S) {
+  constexpr int N = (kMaxE + kFewThreads - 1) / kFewThreads;  // experts a thread
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int e0 = 2 * tid;  // two experts a thread
-  const uint32_t m0 = e0 < a.E ? S.mask[e0] : 0u, m1 = e0 + 1 < a.E ? S.mask[e0 + 1] : 0u;
-  const int n = (((m0 != 0) + (m1 != 0)) << 16) | (__popc(m0) + __popc(m1));
+  uint32_t m[N];
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    m[i] = N * tid + i < a.E ? S.mask[N * tid + i] : 0u;
+    n += ((m[i] != 0) << 16) + __popc(m[i]);
+  }
   int incl = n;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -192,130 +391,219 @@ __device__ void build_active(const FewArgs& a, FewShared& S) {
     if (lane >= o) incl += v;
   }
   if (lane == 31) S.scan[warp] = incl;
-  __syncthreads();
+  sync_consumers();
   int before = (1 << 16) | a.T, total = 0;  // entry 0 and the pairs 0 .. T-1: the shared expert
+#pragma unroll
   for (int i = 0; i < kFewWarps; ++i) {
-    if (i < warp) before += S.scan[i];
-    total += S.scan[i];
+    const int v = S.scan[i];
+    if (i < warp) before += v;
+    total += v;
   }
   before += incl - n;
   int at = before >> 16, pair = before & 0xffff;
-  const uint32_t m[2] = {m0, m1};
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < N; ++i) {
     if (!m[i]) continue;
-    S.act_e[at] = (int16_t)(e0 + i);
+    S.act_e[at] = (int16_t)(N * tid + i);
     S.act_pair[at] = (int16_t)pair;
     S.act_mask[at] = (uint8_t)m[i];
-    S.index[e0 + i] = (uint16_t)at;
+    S.index[N * tid + i] = (uint16_t)at;
     ++at;
     pair += __popc(m[i]);
   }
   if (tid == 0) S.n_act = 1 + (total >> 16);
-  __syncthreads();
+  asm volatile("fence.proxy.async;" ::: "memory");  // the logits' place becomes the ring again
+  ptx::bar_arrive(kBarRouted, kFewBlock);
+  sync_consumers();
   if (tid < a.T * a.k) {
     const int t = tid / a.k, j = tid - t * a.k;
     const int s = S.index[S.sel_e[t][j]];
     S.pair_w[S.act_pair[s] + __popc(S.act_mask[s] & ((1u << t) - 1u))] = S.sel_w[t][j];
   }
-  __syncthreads();
+  sync_consumers();
 }
 
-// Row sums of one 8-channel gate|up tile over this warp's share of the hidden size.
-__device__ __forceinline__ void tile_bf16(const uint8_t* gate, const uint8_t* up, int nk, const uint8_t* xs,
-                                          bool tok, int warp, int t4, float (&acc)[4]) {
-  for (int kb = warp; kb < nk; kb += 4 * kFewWarps) {
-    uint4 wa[4], wb[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (kb + u * kFewWarps < nk) {
-        const size_t at = (size_t)(kb + u * kFewWarps) * 64 + 16 * t4;
-        wa[u] = ld_stream_v4(gate + at);
-        wb[u] = ld_stream_v4(up + at);
-      }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (kb + u * kFewWarps < nk) {
-        uint4 xb = make_uint4(0u, 0u, 0u, 0u);
-        if (tok) xb = *reinterpret_cast<const uint4*>(xs + (size_t)(kb + u * kFewWarps) * 64 + 16 * t4);
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_k32<false>(d, wa[u], wb[u], xb);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] += d[i];
-      }
+// ---------------------------------------------------------------- gate|up
+// Tiles of 8 channels, the shared expert's (s = 0) first, then expert by expert; CTA b takes the
+// tiles b, b + grid, ... in order.
+struct Tiles {
+  int u, s, c;  // tile, its expert's place among the active ones, its place in the expert
+  __device__ void begin() {
+    u = c = blockIdx.x;
+    s = 0;
   }
-}
-
-__device__ __forceinline__ void tile_w4(const uint8_t* gate, const uint8_t* up, const uint16_t* sgp,
-                                        const uint16_t* sup, int nk, int shift, const uint8_t* xs,
-                                        bool tok, int warp, int t4, float (&acc)[4]) {
-  const int nb = (nk + 3) / 4;
-  for (int b = warp; b < nb; b += kFewWarps) {
-    const uint4 wa = ld_stream_v4(gate + (size_t)b * 64 + 16 * t4);
-    const uint4 wb = ld_stream_v4(up + (size_t)b * 64 + 16 * t4);
-    float sa[4], sb[4];
-    w4_block_scales(sgp, b, shift, sa);
-    w4_block_scales(sup, b, shift, sb);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (4 * b + j >= nk) break;
-      uint4 xb = make_uint4(0u, 0u, 0u, 0u);
-      if (tok) xb = *reinterpret_cast<const uint4*>(xs + (size_t)(4 * b + j) * 64 + 16 * t4);
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-      mma_k32<false>(d, w4_pairs<false>((&wa.x)[j]), w4_pairs<false>((&wb.x)[j]), xb);
-      acc[0] = fmaf(d[0], sa[j], acc[0]);
-      acc[1] = fmaf(d[1], sa[j], acc[1]);
-      acc[2] = fmaf(d[2], sb[j], acc[2]);
-      acc[3] = fmaf(d[3], sb[j], acc[3]);
+  __device__ void settle(int ns, int nr) {
+    while (c >= (s ? nr : ns)) {
+      c -= s ? nr : ns;
+      ++s;
     }
   }
-}
+  __device__ void next() {
+    u += gridDim.x;
+    c += gridDim.x;
+  }
+};
 
-// Gate|up tiles [u0, u1) of this CTA's stride: tiles of the shared expert first.
-template <bool W4>
-__device__ void gate_up_tiles(const FewArgs& a, FewShared& S, const uint8_t* xs, int xpitch, int u0,
-                              int u1) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-  const int ns = a.Is / 8, nr = a.I / 8;
-  const bool tok = g < a.T;
-  const uint8_t* xg = xs + (size_t)g * xpitch;
-  int buf = 0;
-  for (int u = u0 + (int)((blockIdx.x + gridDim.x - u0 % gridDim.x) % gridDim.x); u < u1; u += gridDim.x) {
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    int s = 0, c0 = 8 * u;
-    if (u < ns) {
-      const uint8_t* base = reinterpret_cast<const uint8_t*>(a.ws_gate_up);
-      const size_t rb = 2 * (size_t)a.H;
-      tile_bf16(base + (size_t)(c0 + g) * rb, base + (size_t)(a.Is + c0 + g) * rb, a.H / 32, xg, tok,
-                warp, t4, acc);
-    } else {
-      s = 1 + (u - ns) / nr;
-      c0 = 8 * ((u - ns) % nr);
-      const size_t row = (size_t)S.act_e[s] * 2 * a.I + c0 + g;
-      if constexpr (W4) {
-        const size_t rb = w4_row_bytes(a.H), rs = w4_row_scales(a.H, 32 << a.shift);
-        tile_w4(a.gate_up + row * rb, a.gate_up + (row + a.I) * rb, a.s_gate_up + row * rs,
-                a.s_gate_up + (row + a.I) * rs, a.H / 32, a.shift, xg, tok, warp, t4, acc);
+// The weights' feeder; `h`: the feeder of h, which has nothing to add to these stages. Tiles up to
+// tile `end`.
+template <int FMT>
+__device__ void feed_gate_up(Feeder& f, const FewMaps& m, bool h, Tiles& tile, int end) {
+  const FewArgs& a = f.a;
+  for (; tile.u < end; tile.next()) {
+    tile.settle(a.Is / 8, a.I / 8);
+    const bool shared = tile.s == 0, w4 = FMT >= 0 && !shared;
+    const FewChunks& ch = shared ? a.gu_s : a.gu;
+    const int e = shared ? 0 : f.S.act_e[tile.s], c0 = 8 * tile.c;
+    for (int c = 0; c < ch.n; ++c) {
+      uint8_t* dst = f.begin();
+      if (!f.ok) return;
+      uint64_t* bar = &f.S.full[f.cur.s];
+      if (h) {
+        ptx::mbar_arrive(bar);
       } else {
-        const size_t rb = 2 * (size_t)a.H;
-        tile_bf16(a.gate_up + row * rb, a.gate_up + (row + a.I) * rb, a.H / 32, xg, tok, warp, t4, acc);
+        ptx::mbar_arrive_expect_tx(bar, 1024 * ch.cb + (w4 ? 16 * ch.sc : 0));
+        tma_5d(dst, shared ? &m.gu_s : &m.gu, bar, 0, c0, c * ch.cb, 0, e);
+        if (w4) tma_4d(dst + 1024 * ch.cb, &m.gu_sc, bar, c * ch.sc, c0, 0, e);
+      }
+      f.end();
+    }
+  }
+}
+
+// This team's chunks of the tile whose first stage is `first`: this warp's blocks of the gate and the
+// up rows, for 4 NQ tokens. xg: x of the lane's first column, rows of 16-byte words in the order
+// of mma_rows_word. An MMA chain is a stage's blocks at most; stages add up in fp32.
+template <int FMT, int NQ>
+__device__ __forceinline__ void tile_sums(const FewArgs& a, FewShared& S, const FewChunks& ch, uint32_t ring,
+                                          Place& at, int first, uint32_t xg, int xstep, const int (&tok)[NQ],
+                                          int warp, int lane, float (&gate)[NQ][4], float (&up)[NQ][4]) {
+  const int g = lane >> 2, t4 = lane & 3, wt = warp & (kFewTeam - 1);
+  uint2 x[NQ];  // stays zero in the lanes of no token
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) x[q] = make_uint2(0u, 0u);
+  for (; at.i < first + ch.n; at.next(a.stages)) {
+    const uint32_t st = ring + at.cur.s * a.stage_bytes;
+    const int b0 = (at.i - first) * ch.cb, nb = min(ch.cb, ch.blocks - b0);
+    wait_phase(&S.full[at.cur.s], at.cur.parity, S, a.status);
+    uint32_t wp = st + 64 * g + 16 * t4 + 512 * wt;
+    const uint32_t up_at = 512 * ch.cb;
+    if constexpr (FMT >= 0) {
+      uint32_t xp = xg + (b0 + wt) * 256;
+      const uint32_t sp = st + 1024 * ch.cb + g * ch.sc;
+      for (int b = wt; b < nb; b += kFewTeam, wp += 512 * kFewTeam, xp += 256 * kFewTeam) {
+        const uint4 wg = lds_v4(wp), wu = lds_v4(wp + up_at);
+        const uint2 sg = w4_block_scales<FMT>(sp, b), su = w4_block_scales<FMT>(sp + 8 * ch.sc, b);
+        const int parts = min(4, a.H / 32 - 4 * (b0 + b));
+        float dg[NQ][4], du[NQ][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j >= 2 && j >= parts) break;  // H is a multiple of 64: two parts or four
+          const uint4 pg = w4_pairs<false>((&wg.x)[j]), pu = w4_pairs<false>((&wu.x)[j]);
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            lds_v2_if(x[q], xp + q * xstep + 64 * j, tok[q]);
+            // the parts of a group share a chain and a scale
+            if (j % (1 << FMT) == 0) {
+              mma_rows<true>(dg[q], pg, x[q]);
+              mma_rows<true>(du[q], pu, x[q]);
+            } else {
+              mma_rows<false>(dg[q], pg, x[q]);
+              mma_rows<false>(du[q], pu, x[q]);
+            }
+            if ((j + 1) % (1 << FMT) == 0 || (j == 1 && parts == 2)) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                gate[q][i] = fmaf(dg[q][i], w4_scale(sg, j), gate[q][i]);
+                up[q][i] = fmaf(du[q][i], w4_scale(su, j), up[q][i]);
+              }
+            }
+          }
+        }
+      }
+    } else {
+      uint32_t xp = xg + (b0 + wt) * 64;
+      float dg[NQ][4] = {}, du[NQ][4] = {};
+#pragma unroll 5
+      for (int b = wt; b < nb; b += kFewTeam, wp += 512 * kFewTeam, xp += 64 * kFewTeam) {
+        const uint4 wg = lds_v4(wp), wu = lds_v4(wp + up_at);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          lds_v2_if(x[q], xp + q * xstep, tok[q]);
+          mma_rows<false>(dg[q], wg, x[q]);
+          mma_rows<false>(du[q], wu, x[q]);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          gate[q][i] += dg[q][i];
+          up[q][i] += du[q][i];
+        }
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&S.empty[at.cur.s]);
+  }
+}
+
+// The two halves of mma_rows' sums: lane 4 g + t gets weight row g and columns 2 (t & 1) (v0) and
+// 2 (t & 1) + 1 (v1).
+__device__ __forceinline__ void fold(const float (&d)[4], bool low, float& v0, float& v1) {
+  v0 = low ? d[0] : d[2];
+  v1 = low ? d[1] : d[3];
+  v0 += __shfl_xor_sync(0xffffffffu, v0, 2);
+  v1 += __shfl_xor_sync(0xffffffffu, v1, 2);
+}
+
+// `stage`: the number of the first tile's first stage, on return that behind the last.
+template <int FMT, int NQ>
+__device__ __forceinline__ void gate_up_tiles(const FewArgs& a, FewShared& S, uint32_t xs, int xpitch,
+                                              uint32_t ring, Place& at, int& stage, Tiles& tile, int end) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+  int tok[NQ];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) tok[q] = 4 * q + (g & 3) < a.T;
+  const uint32_t xg = xs + (g & 3) * xpitch + 16 * t4 + 8 * (g >> 2);
+  int buf = 0, turn = 0;
+  for (; tile.u < end; tile.next()) {
+    tile.settle(a.Is / 8, a.I / 8);
+    float gate[NQ][4] = {}, up[NQ][4] = {};
+    const int s = tile.s, c0 = 8 * tile.c;
+    if (s == 0) {
+      tile_sums<-1, NQ>(a, S, a.gu_s, ring, at, stage, xg, 4 * xpitch, tok, warp, lane, gate, up);
+      stage += a.gu_s.n;
+    } else {
+      tile_sums<FMT, NQ>(a, S, a.gu, ring, at, stage, xg, 4 * xpitch, tok, warp, lane, gate, up);
+      stage += a.gu.n;
+    }
+    float* red = S.red[buf][warp];  // [gate, up][token][channel]
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      float g0, g1, v0, v1;
+      fold(gate[q], t4 < 2, g0, g1);
+      fold(up[q], t4 < 2, v0, v1);
+      float* to = red + 8 * (4 * q + 2 * (t4 & 1)) + g;
+      if (t4 < 2) {
+        to[0] = g0;
+        to[8] = g1;
+      } else {
+        to[64] = v0;
+        to[72] = v1;
       }
     }
-    float* red = S.red[buf][warp];
-    *reinterpret_cast<float2*>(red + 8 * g + 2 * t4) = make_float2(acc[0], acc[1]);
-    *reinterpret_cast<float2*>(red + 8 * (g + 8) + 2 * t4) = make_float2(acc[2], acc[3]);
-    __syncthreads();
-    if (tid < 64) {
-      const int t = tid >> 3, c = tid & 7;
+    sync_consumers();
+    if (warp >> 1 == turn) {  // a pair of warps finishes the tile, another pair the next one
+      const int at64 = tid & 63, t = at64 >> 3, c = at64 & 7;
       const uint32_t m = s ? S.act_mask[s] : (1u << a.T) - 1u;
       if ((m >> t) & 1u) {
         float gate = 0.f, up = 0.f;
+#pragma unroll
         for (int w = 0; w < kFewWarps; ++w) {
-          gate += S.red[buf][w][8 * c + t];
-          up += S.red[buf][w][8 * (c + 8) + t];
+          gate += S.red[buf][w][at64];
+          up += S.red[buf][w][64 + at64];
         }
         const int pair = s ? S.act_pair[s] + __popc(m & ((1u << t) - 1u)) : t;
-        const float h = gate / (1.f + expf(-gate)) * up * (s ? S.pair_w[pair] : S.sgate[t]);
+        const float h = gate / (1.f + expf(-gate)) * up * (s ? S.pair_w[pair] : 1.f);
         // three truncated pieces: 8 + 8 + 8 significant bits, h exactly (an infinity or NaN in
         // the first alone)
         const uint32_t hb = __float_as_uint(h);
@@ -323,184 +611,436 @@ __device__ void gate_up_tiles(const FewArgs& a, FewShared& S, const uint8_t* xs,
         const float r1 = fin ? h - __uint_as_float(hb & 0xffff0000u) : 0.f;
         const uint32_t mb = __float_as_uint(r1);
         const float r2 = r1 - __uint_as_float(mb & 0xffff0000u);
-        uint16_t* o = a.h + (size_t)pair * a.ldh + c0 + c;
+        const int ch = c0 + c;
+        uint16_t* o = a.h + ((size_t)pair * (a.ldh / 32) + ch / 32) * 96 + (ch % 32 & ~7) +
+                      2 * mma_rows_word(ch % 8 / 2) + ch % 2;
         o[0] = (h == h) ? (uint16_t)(hb >> 16) : (uint16_t)0x7fc0u;
-        o[a.h_plane] = (uint16_t)(mb >> 16);
-        o[2 * a.h_plane] = (uint16_t)(__float_as_uint(r2) >> 16);
+        o[32] = (uint16_t)(mb >> 16);
+        o[64] = (uint16_t)(__float_as_uint(r2) >> 16);
+        asm volatile("fence.proxy.async.global;" ::: "memory");  // h is read by bulk copies
       }
     }
     buf ^= 1;  // the next tile's sums go to the other half: one barrier a tile is enough
+    turn = turn + 1 == kFewWarps / 2 ? 0 : turn + 1;
   }
 }
 
-template <bool W4>
-__device__ void down_rows(const FewArgs& a, FewShared& S) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-  const int n0 = (int)((int64_t)blockIdx.x * a.H / gridDim.x);
-  const int n1 = (int)((int64_t)(blockIdx.x + 1) * a.H / gridDim.x);
-  float* red = &S.red[0][0][0];  // [warp][row][token]
-  for (int r0 = n0; r0 < n1; r0 += kFewRows) {
-    const int nr = min(kFewRows, n1 - r0);
-    float acc[2][4] = {};
-    int turn = 0;  // the blocks of all experts go to the warps in turn
+// ---------------------------------------------------------------- down
+// CTA b owns the output rows [b H / grid, (b + 1) H / grid), a.rows (at most 32) in a pass.
+__device__ __forceinline__ int row_begin(const FewArgs& a, int b) { return (int)((int64_t)b * a.H / gridDim.x); }
+
+template <int FMT>
+__device__ void feed_down(Feeder& f, const FewMaps& m) {
+  const FewArgs& a = f.a;
+  const int n1 = row_begin(a, blockIdx.x + 1);
+  for (int r0 = row_begin(a, blockIdx.x); r0 < n1; r0 += a.rows)
+    for (int s = 0; s < f.S.n_act; ++s) {
+      const FewChunks& ch = s ? a.dn : a.dn_s;
+      const int e = s ? f.S.act_e[s] : 0, bytes = a.rows * 64 * ch.cb;
+      for (int c = 0; c < ch.n; ++c) {
+        uint8_t* dst = f.begin();
+        if (!f.ok) return;
+        uint64_t* bar = &f.S.full[f.cur.s];
+        const bool w4 = FMT >= 0 && s;
+        ptx::mbar_arrive_expect_tx(bar, bytes + (w4 ? a.rows * ch.sc : 0));
+        tma_4d(dst, s ? &m.dn : &m.dn_s, bar, 0, r0, c * ch.cb, e);
+        if (w4) tma_3d(dst + round128(bytes), &m.dn_sc, bar, c * ch.sc, r0, e);
+        f.end();
+      }
+    }
+}
+
+// h for the same stages, once all of it is there.
+template <int FMT>
+__device__ void feed_h(Feeder& f, uint8_t* units) {
+  const FewArgs& a = f.a;
+  FewShared& S = f.S;
+  grid_wait(a.sync + 1, S, a.status);
+  asm volatile("fence.proxy.async;" ::: "memory");
+  const int n1 = row_begin(a, blockIdx.x + 1);
+  Cursor done = f.cur;  // the oldest stage whose units are not known to be free
+  int flight = 0, in_use = 0, at = 0;
+  auto pop = [&] {
+    in_use -= S.stage_units[done.s];
+    done.next(a.stages);
+    --flight;
+  };
+  for (int r0 = row_begin(a, blockIdx.x); r0 < n1; r0 += a.rows)
     for (int s = 0; s < S.n_act; ++s) {
-      const bool w4 = W4 && s > 0;
-      const int K = s ? a.I : a.Is;
-      const int nk = K / 32, n = w4 ? (nk + 3) / 4 : nk;
-      const uint32_t m = s ? S.act_mask[s] : (1u << a.T) - 1u;
-      const bool tok = (m >> g) & 1u;
-      const bool c0 = (m >> (2 * t4)) & 1u, c1 = (m >> (2 * t4 + 1)) & 1u;
-      const int pair = (s ? S.act_pair[s] : 0) + __popc(m & ((1u << g) - 1u));
-      const uint8_t* h = reinterpret_cast<const uint8_t*>(a.h + (size_t)pair * a.ldh) + 16 * t4;
-      const size_t row = s ? (size_t)S.act_e[s] * a.H + r0 + g : (size_t)(r0 + g);
-      const size_t rb = w4 ? (size_t)w4_row_bytes(K) : 2 * (size_t)K;
-      const uint8_t* base = (s ? a.down : reinterpret_cast<const uint8_t*>(a.ws_down)) + row * rb + 16 * t4;
-      for (int b = (warp + kFewWarps - turn) % kFewWarps; b < n; b += kFewWarps) {
-        uint4 w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t zero = w4 ? 0x88888888u : 0u;
-          w[i] = make_uint4(zero, zero, zero, zero);
-          if (g + 8 * i < nr) w[i] = ld_stream_v4(base + 8 * i * rb + (size_t)b * 64);
+      const FewChunks& ch = s ? a.dn : a.dn_s;
+      const int nt = s ? __popc(S.act_mask[s]) : a.T;
+      const int block = FMT >= 0 && s ? 768 : 192, total = 6 * (s ? a.I : a.Is);
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(a.h) + (s ? (size_t)S.act_pair[s] : 0) * a.ldh * 6;
+      for (int c = 0; c < ch.n; ++c) {
+        f.begin();
+        if (f.ok && flight == a.stages) pop();  // it was in this place
+        while (f.ok && in_use + nt > a.units) {
+          f.ok = wait_phase(&S.empty[done.s], done.parity, S, a.status);
+          pop();
         }
-        auto part = [&](int kb, const uint4& xa, const uint4& xb, int i, float s0, float s1) {
-          uint4 hp[3] = {};
-          if (tok)
+        if (!f.ok) return;
+        const int from = c * ch.cb * block, n = min(ch.cb * block, total - from);
+        uint64_t* bar = &S.full[f.cur.s];
+        ptx::mbar_arrive_expect_tx(bar, nt * n);
+        for (int q = 0; q < nt; ++q) {
+          bulk_load(units + (size_t)at * a.unit, src + (size_t)q * a.ldh * 6 + from, n, bar);
+          if (++at == a.units) at = 0;
+        }
+        S.stage_units[f.cur.s] = (uint8_t)nt;
+        in_use += nt;
+        ++flight;
+        f.end();
+      }
+    }
+}
+
+// One expert's chunks, W_down times h of its tokens, for N of them (the ranks `rank` on among the
+// expert's tokens) at a time. A token's three pieces are the MMA's columns 0-2 (and 4-6), column 3 is
+// zero. acc[tile][0], [1]: row 8 tile + g, the tokens t and t + 4 in lane 4 g + t.
+template <int FMT, int NI, int N>
+__device__ __forceinline__ void expert_blocks(const FewArgs& a, const FewChunks& ch, uint32_t st, uint32_t units,
+                                              int unit, uint32_t mask, int b0, int nb, int K, int nr, int wt,
+                                              int lane, float (&acc)[NI][2]) {
+  const int g = lane >> 2, t4 = lane & 3, piece = (g & 3) < 3;
+  // rows behind the pass read its last one: only the last tile can have any
+  const uint32_t row = 64 * g + 16 * t4, last = 64 * min(8 * (NI - 1) + g, nr - 1) + 16 * t4;
+  uint32_t wp = st + 64 * wt * a.rows, hu[N];
+  uint2 x[N];
 #pragma unroll
-            for (int p = 0; p < 3; ++p) hp[p] = ld_cg_v4(h + 2 * p * a.h_plane + (size_t)kb * 64);
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int n = 0; n < N; ++n) {
+    int u = unit + n;
+    if (u >= a.units) u -= a.units;
+    hu[n] = units + u * a.unit + 64 * (g & 3) + 16 * t4 + 8 * (g >> 2) + wt * (FMT >= 0 ? 768 : 192);
+    x[n] = make_uint2(0u, 0u);
+  }
+  float sum[N][NI][4] = {};
+  if constexpr (FMT >= 0) {
+    const uint32_t sp = st + round128(a.rows * 64 * ch.cb);
+    for (int b = wt; b < nb; b += kFewTeam, wp += 64 * kFewTeam * a.rows) {
+      uint4 w[NI];
+      uint2 sc[NI];
 #pragma unroll
-          for (int p = 2; p >= 0; --p) mma_k32<false>(d, xa, xb, hp[p]);  // small pieces first
-          if (c0) {
-            acc[i][0] = fmaf(d[0], s0, acc[i][0]);
-            acc[i][2] = fmaf(d[2], s1, acc[i][2]);
+      for (int i = 0; i < NI; ++i) {
+        w[i] = lds_v4(wp + (i < NI - 1 ? row + 512 * i : last));
+        sc[i] = w4_block_scales<FMT>(sp + (i < NI - 1 ? 8 * i + g : min(8 * i + g, nr - 1)) * ch.sc, b);
+      }
+      const int parts = min(4, K / 32 - 4 * (b0 + b));
+      float d[N][NI][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j >= 2 && j >= parts) break;  // K is a multiple of 64: two parts or four
+#pragma unroll
+        for (int n = 0; n < N; ++n) lds_v2_if(x[n], hu[n] + 192 * j, piece);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const uint4 pw = w4_pairs<false>((&w[i].x)[j]);
+          const float f = w4_scale(sc[i], j);
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            // the parts of a group share a chain and a scale
+            if (j % (1 << FMT) == 0) mma_rows<true>(d[n][i], pw, x[n]);
+            else mma_rows<false>(d[n][i], pw, x[n]);
+            if ((j + 1) % (1 << FMT) == 0 || (j == 1 && parts == 2))
+#pragma unroll
+              for (int q = 0; q < 4; ++q) sum[n][i][q] = fmaf(d[n][i][q], f, sum[n][i][q]);
           }
-          if (c1) {
-            acc[i][1] = fmaf(d[1], s0, acc[i][1]);
-            acc[i][3] = fmaf(d[3], s1, acc[i][3]);
-          }
-        };
-        if (W4 && w4) {
-          float sc[4][4] = {};
-          const size_t rs = w4_row_scales(K, 32 << a.shift);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (g + 8 * i < nr) w4_block_scales(a.s_down + (row + 8 * i) * rs, b, a.shift, sc[i]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (4 * b + j >= nk) break;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              part(4 * b + j, w4_pairs<false>((&w[2 * i].x)[j]), w4_pairs<false>((&w[2 * i + 1].x)[j]), i,
-                   sc[2 * i][j], sc[2 * i + 1][j]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) part(b, w[2 * i], w[2 * i + 1], i, 1.f, 1.f);
         }
       }
-      turn = (turn + n) % kFewWarps;
+#pragma unroll
+      for (int n = 0; n < N; ++n) hu[n] += 768 * kFewTeam;
     }
-    __syncthreads();
+  } else {
+#pragma unroll 5
+    for (int b = wt; b < nb; b += kFewTeam, wp += 64 * kFewTeam * a.rows) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int n = 0; n < N; ++n) {
+        lds_v2_if(x[n], hu[n], piece);
+        hu[n] += 192 * kFewTeam;
+      }
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
-        *reinterpret_cast<float2*>(red + (warp * kFewRows + 16 * i + 8 * p + g) * kFewMaxT + 2 * t4) =
-            make_float2(acc[i][2 * p], acc[i][2 * p + 1]);
-    __syncthreads();
-    const int r = tid % kFewRows, t = tid / kFewRows;
-    float sum = 0.f;
-    if (t < kFewMaxT)
-      for (int w = 0; w < kFewWarps; ++w) sum += red[(w * kFewRows + r) * kFewMaxT + t];
-    if (t < a.T && r < nr) a.out[(size_t)t * a.H + r0 + r] = sum;
+      for (int i = 0; i < NI; ++i) {
+        const uint4 w = lds_v4(wp + (i < NI - 1 ? row + 512 * i : last));
+#pragma unroll
+        for (int n = 0; n < N; ++n) mma_rows<false>(sum[n][i], w, x[n]);
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int token = __ffs(mask) - 1;
+    mask &= mask - 1;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      float v0, v1;
+      fold(sum[n][i], t4 < 2, v0, v1);
+      float v = v0 + (t4 & 1 ? 0.f : v1);  // third piece, or first and second
+      v += __shfl_xor_sync(0xffffffffu, v, 1);
+      if ((token & 3) == t4) {
+        if (token < 4) acc[i][0] += v;
+        else acc[i][1] += v;
+      }
+    }
   }
 }
 
-template <bool W4>
-__global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewArgs a) {
-  extern __shared__ uint4 smem[];
-  FewShared& S = *reinterpret_cast<FewShared*>(smem);
-  uint8_t* xs = reinterpret_cast<uint8_t*>(smem) + (sizeof(FewShared) + 127) / 128 * 128;
-  const int xpitch = 2 * a.H + 64;  // 64 mod 128: two tokens' 64-byte reads share no bank
+template <int FMT, int NI>
+__device__ __forceinline__ void expert_sums(const FewArgs& a, FewShared& S, const FewChunks& ch, uint32_t ring,
+                                            Place& at, int first, uint32_t units, int unit, int K, uint32_t mask,
+                                            int nr, int warp, int lane, float (&acc)[NI][2]) {
+  const int wt = warp & (kFewTeam - 1), nt = __popc(mask);
+  for (; at.i < first + ch.n; at.next(a.stages)) {
+    const uint32_t st = ring + at.cur.s * a.stage_bytes;
+    const int c = at.i - first, b0 = c * ch.cb, nb = min(ch.cb, ch.blocks - b0);
+    int u = unit + c * nt;
+    while (u >= a.units) u -= a.units;
+    wait_phase(&S.full[at.cur.s], at.cur.parity, S, a.status);
+    uint32_t left = mask;
+    while (left & (left - 1)) {  // two tokens at a time
+      expert_blocks<FMT, NI, 2>(a, ch, st, units, u, left, b0, nb, K, nr, wt, lane, acc);
+      left &= left - 1;
+      left &= left - 1;
+      u += 2;
+      if (u >= a.units) u -= a.units;
+    }
+    if (left) expert_blocks<FMT, NI, 1>(a, ch, st, units, u, left, b0, nb, K, nr, wt, lane, acc);
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&S.empty[at.cur.s]);
+  }
+}
+
+// One pass of NI row tiles.
+template <int FMT, int NI>
+__device__ __forceinline__ void down_pass(const FewArgs& a, FewShared& S, uint32_t ring, Place& at, int& stage,
+                                          uint32_t units, int& unit, int nr, int warp, int lane) {
+  const int g = lane >> 2, t4 = lane & 3;
+  float acc[NI][2] = {};
+  expert_sums<-1, NI>(a, S, a.dn_s, ring, at, stage, units, unit, a.Is, (1u << a.T) - 1u, nr, warp, lane, acc);
+  stage += a.dn_s.n;
+  for (unit += a.dn_s.n * a.T; unit >= a.units;) unit -= a.units;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {  // the shared expert's gate
+    acc[i][0] *= S.sgate[t4];
+    acc[i][1] *= S.sgate[4 + t4];
+  }
+  for (int s = 1; s < S.n_act; ++s) {
+    const uint32_t m = S.act_mask[s];
+    if (at.i < stage + a.dn.n)  // this team has a stage of the expert
+      expert_sums<FMT, NI>(a, S, a.dn, ring, at, stage, units, unit, a.I, m, nr, warp, lane, acc);
+    stage += a.dn.n;
+    for (unit += a.dn.n * __popc(m); unit >= a.units;) unit -= a.units;
+  }
+  float* red = &S.red[0][0][0];  // [warp][row][token]
+  sync_consumers();
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    float* to = red + (warp * kFewRows + 8 * i + g) * kFewMaxT + t4;
+    to[0] = acc[i][0];
+    to[4] = acc[i][1];
+  }
+}
+
+template <int FMT>
+__device__ void down_rows(const FewArgs& a, FewShared& S, uint32_t ring, Place& at, int stage, uint32_t units) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-
-  for (int i = tid; i < a.T * (a.H / 8); i += kFewThreads) {
-    const int t = i / (a.H / 8), c = i - t * (a.H / 8);
-    *reinterpret_cast<uint4*>(xs + (size_t)t * xpitch + 16 * c) = ld_v4(a.x + (size_t)t * a.H + 8 * c);
-  }
-  for (int e = tid; e < a.E; e += kFewThreads) S.mask[e] = 0;
-  __syncthreads();
-
-  // logits of this CTA's router rows, four at a time; a warp takes a slice of the hidden size
-  const int e0 = (int)((int64_t)blockIdx.x * a.E / gridDim.x);
-  const int e1 = (int)((int64_t)(blockIdx.x + 1) * a.E / gridDim.x);
-  for (int e = e0; e < e1; e += 4) {
-    double acc[4][kFewMaxT] = {};
-    for (int c = warp * 32 + lane; c < a.H; c += kFewThreads) {
-      float w[4];
+  const float* red = &S.red[0][0][0];
+  const int n1 = row_begin(a, blockIdx.x + 1);
+  int unit = 0;
+  for (int r0 = row_begin(a, blockIdx.x); r0 < n1; r0 += a.rows) {
+    const int nr = min(a.rows, n1 - r0);
+    if (nr > 24) down_pass<FMT, 4>(a, S, ring, at, stage, units, unit, nr, warp, lane);
+    else if (nr > 16) down_pass<FMT, 3>(a, S, ring, at, stage, units, unit, nr, warp, lane);
+    else if (nr > 8) down_pass<FMT, 2>(a, S, ring, at, stage, units, unit, nr, warp, lane);
+    else down_pass<FMT, 1>(a, S, ring, at, stage, units, unit, nr, warp, lane);
+    sync_consumers();
+    const int r = tid % kFewRows, t = tid / kFewRows;
+    if (t < a.T && r < nr) {
+      float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = e + i < e1 ? __ldg(a.w_router + (size_t)(e + i) * a.H + c) : 0.f;
-#pragma unroll
-      for (int t = 0; t < kFewMaxT; ++t)
-        if (t < a.T) {
-          const uint32_t b = *reinterpret_cast<const uint16_t*>(xs + (size_t)t * xpitch + 2 * c);
-          const double xv = (double)__uint_as_float(b << 16);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i][t] = fma((double)w[i], xv, acc[i][t]);
-        }
+      for (int w = 0; w < kFewWarps; ++w) sum += red[(w * kFewRows + r) * kFewMaxT + t];
+      a.out[(size_t)t * a.H + r0 + r] = sum;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int t = 0; t < kFewMaxT; ++t)
-        if (t < a.T) {
-          double v = acc[i][t];
-#pragma unroll
-          for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-          if (lane == 0) S.part[warp][i * kFewMaxT + t] = v;
-        }
-    __syncthreads();
-    if (tid < 32) {
-      const int i = tid / kFewMaxT, t = tid % kFewMaxT;
-      if (t < a.T && e + i < e1) {
-        double v = 0.0;
-        for (int w = 0; w < kFewWarps; ++w) v += S.part[w][tid];
-        a.logits[(size_t)t * a.E + e + i] = v;
+  }
+}
+
+// ---------------------------------------------------------------- router
+// The CTA's rows [e0, e1) of the router matrix (row E: the shared expert's gate vector, bf16), the
+// first stages of the ring: a stage is a row's next stage_bytes / 4 elements.
+struct RouterRows {
+  int e0, e1, chunk, n;
+};
+__device__ __forceinline__ RouterRows router_rows(const FewArgs& a) {
+  RouterRows r;
+  r.e0 = (int)((int64_t)blockIdx.x * (a.E + 1) / gridDim.x);
+  r.e1 = (int)((int64_t)(blockIdx.x + 1) * (a.E + 1) / gridDim.x);
+  r.chunk = a.stage_bytes / 4;
+  r.n = (a.H + r.chunk - 1) / r.chunk;
+  return r;
+}
+
+__device__ void feed_router(Feeder& f, uint8_t* xs, int xpitch, bool h) {
+  const FewArgs& a = f.a;
+  if (!h) {
+    ptx::mbar_arrive_expect_tx(&f.S.x_full, 2 * a.T * a.H);
+    for (int t = 0; t < a.T; ++t) bulk_load(xs + (size_t)t * xpitch, a.x + (size_t)t * a.H, 2 * a.H, &f.S.x_full);
+  }
+  const RouterRows r = router_rows(a);
+  for (int e = r.e0; e < r.e1; ++e)
+    for (int c = 0; c < r.n; ++c) {
+      uint8_t* dst = f.begin();
+      if (!f.ok) return;
+      uint64_t* bar = &f.S.full[f.cur.s];
+      if (h) {
+        ptx::mbar_arrive(bar);
+      } else {
+        const int k = c * r.chunk, n = min(r.chunk, a.H - k);
+        const bool gate = e == a.E;
+        const void* src = gate ? static_cast<const void*>(a.wsg + k) : a.w_router + (size_t)e * a.H + k;
+        ptx::mbar_arrive_expect_tx(bar, n * (gate ? 2 : 4));
+        bulk_load(dst, src, n * (gate ? 2 : 4), bar);
       }
+      f.end();
     }
-    __syncthreads();
+}
+
+// Sums of N values a lane over the warp by recursive halving: lane l gets value l >> (5 - log2 N).
+template <int N>
+__device__ __forceinline__ double warp_sums(double (&v)[N], int lane) {
+  int off = 16;
+#pragma unroll
+  for (int n = N / 2; n >= 1; n /= 2, off /= 2) {
+    const bool upper = (lane & off) != 0;
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const double send = upper ? v[j] : v[j + n], keep = upper ? v[j + n] : v[j];
+      v[j] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+    }
   }
+  for (; off >= 1; off /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+  return v[0];
+}
+
+// Logits, in 64 bits: a team takes a stage, a thread four elements at a time. TT: tokens, rounded
+// up to a power of two.
+template <int TT>
+__device__ __forceinline__ void router_logits(const FewArgs& a, FewShared& S, uint8_t* xs, int xpitch,
+                                              const uint8_t* ring, Place& at, int& stage) {
+  constexpr int log_t = TT == 1 ? 0 : TT == 2 ? 1 : TT == 4 ? 2 : 3;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, in_team = tid & (32 * kFewTeam - 1);
+  const RouterRows r = router_rows(a);
+  const int end = (r.e1 - r.e0) * r.n;
+  const int my_e = r.e0 + tid / a.T, my_t = tid % a.T;  // the logit that this thread adds up
+  const bool mine = my_e < r.e1;
+  const float bias = mine && my_e < a.E && a.bias ? __ldg(a.bias + my_e) : 0.f;
+  wait_phase(&S.x_full, 0u, S, a.status);
+  for (; at.i < end; at.next(a.stages)) {
+    const uint8_t* st = ring + (size_t)at.cur.s * a.stage_bytes;
+    const int c = at.i % r.n, k0 = c * r.chunk, n = min(r.chunk, a.H - k0);
+    const bool gate = r.e0 + at.i / r.n == a.E;
+    double acc[TT] = {};
+    wait_phase(&S.full[at.cur.s], at.cur.parity, S, a.status);
+    for (int k = 4 * in_team; k < n; k += 128 * kFewTeam) {
+      float w[4];
+      if (gate) {
+        const uint2 v = *reinterpret_cast<const uint2*>(st + 2 * k);
+        w[0] = bf16lo(v.x); w[1] = bf16hi(v.x); w[2] = bf16lo(v.y); w[3] = bf16hi(v.y);
+      } else {
+        const float4 v = *reinterpret_cast<const float4*>(st + 4 * k);
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+      }
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+        if (t < a.T) {
+          const uint2 v = *reinterpret_cast<const uint2*>(xs + (size_t)t * xpitch + 2 * (k0 + k));
+          acc[t] = fma((double)w[0], (double)bf16lo(v.x), acc[t]);
+          acc[t] = fma((double)w[1], (double)bf16hi(v.x), acc[t]);
+          acc[t] = fma((double)w[2], (double)bf16lo(v.y), acc[t]);
+          acc[t] = fma((double)w[3], (double)bf16hi(v.y), acc[t]);
+        }
+    }
+    const double v = warp_sums<TT>(acc, lane);
+    const int t = lane >> (5 - log_t);
+    if ((lane & ((32 >> log_t) - 1)) == 0 && t < a.T)
+      S.part[(at.i * kFewTeam + (warp & (kFewTeam - 1))) * a.T + t] = v;
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&S.empty[at.cur.s]);
+  }
+  stage = end;
+  sync_consumers();
+  // x for mma_rows from here on: the words of 16 bytes in the order 0, 2, 1, 3
+  for (int i = tid; i < a.T * (a.H / 8); i += kFewThreads) {
+    const int t = i / (a.H / 8);
+    uint2* p = reinterpret_cast<uint2*>(xs + (size_t)t * xpitch + 16 * (i - t * (a.H / 8)));
+    const uint2 lo = p[0], hi = p[1];
+    p[0] = make_uint2(lo.x, hi.x);
+    p[1] = make_uint2(lo.y, hi.y);
+  }
+  if (mine) {
+    double l = 0.0;
+    for (int c = 0; c < r.n; ++c)
+#pragma unroll
+      for (int w = 0; w < kFewTeam; ++w)
+        l += S.part[(((my_e - r.e0) * r.n + c) * kFewTeam + w) * a.T + my_t];
+    a.logits[(size_t)my_t * a.ldl + my_e] = l + (double)bias;
+    asm volatile("fence.proxy.async.global;" ::: "memory");  // read by bulk copies
+  }
+}
+
+// ---------------------------------------------------------------- the kernel
+// All logits are there: every CTA chooses the experts of all tokens for itself. The ring holds
+// nothing now (the feeders wait for the experts) and takes the logits.
+__device__ void route(const FewArgs& a, FewShared& S, uint8_t* ring, int warp, int lane) {
+  sync_consumers();  // the last tile's sums are read: S.cand shares their place
+  if (threadIdx.x == 0) {
+    grid_wait(a.sync, S, a.status);
+    asm volatile("fence.proxy.async;" ::: "memory");
+    ptx::mbar_arrive_expect_tx(&S.logits_full, 8 * a.T * a.ldl);
+    bulk_load(ring, a.logits, 8 * a.T * a.ldl, &S.logits_full);
+  }
+  wait_phase(&S.logits_full, 0u, S, a.status);
+  const double* row = reinterpret_cast<const double*>(ring);
+  if (threadIdx.x >= kFewThreads - 32 && lane < a.T)
+    S.sgate[lane] = 1.f / (1.f + expf(-(float)row[lane * a.ldl + a.E]));
+  if (warp < a.T) {
+    row += warp * a.ldl;
+    if (a.E <= 64) select_token<2>(a, S, row, warp, lane);
+    else if (a.E <= 512) select_token<16>(a, S, row, warp, lane);
+    else select_token<32>(a, S, row, warp, lane);
+  }
+  sync_consumers();
+  build_active(a, S);
+}
+
+template <int FMT>
+__device__ void consume(const FewArgs& a, FewShared& S, uint8_t* xs, int xpitch, uint8_t* ring) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Place at{warp / kFewTeam, {0, 0u}};
+  for (at.cur.s = at.i; at.cur.s >= a.stages; at.cur.s -= a.stages) at.cur.parity ^= 1u;
+  int stage = 0;
+  for (int e = tid; e < a.E; e += kFewThreads) S.mask[e] = 0;
+  if (tid < kFewMaxT) S.sgate[tid] = 0.f;
+  if (a.T == 1) router_logits<1>(a, S, xs, xpitch, ring, at, stage);
+  else if (a.T <= 4) router_logits<4>(a, S, xs, xpitch, ring, at, stage);
+  else router_logits<8>(a, S, xs, xpitch, ring, at, stage);
   grid_arrive(a.sync);
 
-  // the shared expert: its output gate, then its gate|up tiles
-  if (warp < a.T) {
-    float v = 0.f;
-    const uint8_t* xr = xs + (size_t)warp * xpitch;
-    for (int c = lane; c < a.H / 8; c += 32) {
-      float xf[8];
-      unpack8(*reinterpret_cast<const uint4*>(xr + 16 * c), xf);
-      v = dot8_acc(ld_v4(a.wsg + 8 * c), xf, v);
+  const uint32_t xs_at = ptx::smem_u32(xs), ring_at = ptx::smem_u32(ring);
+  Tiles tile;
+  tile.begin();
+  int end = a.Is / 8;  // the shared expert's gate|up tiles need no routing
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass) {
+      route(a, S, ring, warp, lane);
+      end += (S.n_act - 1) * (a.I / 8);
     }
-    v = warp_sum(v);
-    if (lane == 0) S.sgate[warp] = 1.f / (1.f + expf(-v));
+    if (a.T <= 4) gate_up_tiles<FMT, 1>(a, S, xs_at, xpitch, ring_at, at, stage, tile, end);
+    else gate_up_tiles<FMT, 2>(a, S, xs_at, xpitch, ring_at, at, stage, tile, end);
   }
-  __syncthreads();
-  const int ns = a.Is / 8;
-  gate_up_tiles<W4>(a, S, xs, xpitch, 0, ns);
 
-  grid_wait(a.sync, a.status);
-  if (warp < a.T) select_token(a, S, warp, lane);
-  __syncthreads();
-  build_active(a, S);
-  gate_up_tiles<W4>(a, S, xs, xpitch, ns, ns + (S.n_act - 1) * (a.I / 8));
-
+  // h of this CTA is written; that of the others comes through the ring
   grid_arrive(a.sync + 1);
-  grid_wait(a.sync + 1, a.status);
-  down_rows<W4>(a, S);
+  down_rows<FMT>(a, S, ring_at, at, stage, xs_at);
 
   // the last CTA to leave makes the counters ready for the next call
-  __syncthreads();
   if (tid == 0) {
     __threadfence();
     if (atomicAdd(a.sync + 2, 1u) + 1 == gridDim.x) {
@@ -511,11 +1051,111 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewArgs
   }
 }
 
+// Warp 16 feeds weights, warp 17 h; one thread of each.
+template <int FMT>
+__device__ void feed(const FewArgs& a, const FewMaps& m, FewShared& S, uint8_t* ring, uint8_t* xs, int xpitch) {
+  const int lane = threadIdx.x & 31;
+  const bool h = threadIdx.x >= kFewThreads + 32;
+  Feeder f{a, S, ring, Cursor{0, 0u}, 0, true};
+  Tiles tile;
+  tile.begin();
+  const int ns = a.Is / 8;
+  if (lane == 0) {
+    feed_router(f, xs, xpitch, h);
+    feed_gate_up<FMT>(f, m, h, tile, ns);
+  }
+  __syncwarp();
+  ptx::bar_sync(kBarRouted, kFewBlock);
+  if (lane != 0) return;
+  feed_gate_up<FMT>(f, m, h, tile, ns + (S.n_act - 1) * (a.I / 8));
+  if (h) feed_h<FMT>(f, xs);
+  else feed_down<FMT>(f, m);
+  f.drain();
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kFewBlock, 1)
+few_layer_kernel(const __grid_constant__ FewArgs a, const __grid_constant__ FewMaps m) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  FewShared& S = *reinterpret_cast<FewShared*>(smem);
+  uint8_t* xs = smem + kFewSharedBytes;  // x, then the units of h
+  const int xpitch = 2 * a.H + 64;  // 64 mod 128: two tokens' 64-byte reads share no bank
+  uint8_t* ring = xs + a.h_bytes;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      ptx::mbar_init(&S.full[i], 2);
+      ptx::mbar_init(&S.empty[i], kFewTeam);
+    }
+    ptx::mbar_init(&S.x_full, 1);
+    ptx::mbar_init(&S.logits_full, 1);
+    S.aborted = 0;
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  if (threadIdx.x < kFewThreads) consume<FMT>(a, S, xs, xpitch, ring);
+  else feed<FMT>(a, m, S, ring, xs, xpitch);
+}
+
 }  // namespace
 
 bool few_supported(const moe_shape& s) {
   return s.T <= kFewMaxT && (int64_t)s.T * s.H <= kFewMaxTH;
 }
+
+namespace {
+
+// Chunks of a row of K weights for stages of `stage` bytes with `rows` rows, at most `limit` blocks.
+FewChunks few_chunks(int K, int rows, bool w4, int shift, int stage, int limit) {
+  FewChunks c;
+  c.blocks = w4 ? (int)w4_blocks(K) : K / 32;
+  const int per = rows * (64 + (w4 ? 8 >> shift : 0));
+  const int most = std::min((stage - 128 - (w4 ? 16 * rows : 0)) / per, limit);
+  c.n = (c.blocks + most - 1) / most;
+  c.cb = (c.blocks + c.n - 1) / c.n;
+  if (w4 && c.n > 1) {  // a chunk's scales start on 16 bytes
+    const int unit = 2 << shift;
+    c.cb = (c.cb + unit - 1) / unit * unit;
+    if (c.cb > most) c.cb = most / unit * unit;
+  }
+  c.n = (c.blocks + c.cb - 1) / c.cb;
+  c.sc = w4 ? ((c.cb * 8 >> shift) + 15) / 16 * 16 : 0;
+  return c;
+}
+
+bool few_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+             const uint32_t* box) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [64][n][blocks][halves][E] of E matrices of halves * n rows of `row` bytes
+bool few_weight_map(CUtensorMap* m, const void* base, uint64_t n, const FewChunks& c, uint64_t row, uint64_t halves,
+                    uint64_t E, uint32_t box_rows) {
+  const uint64_t dims[5] = {64, n, (uint64_t)c.blocks, halves, E};
+  const uint64_t strides[4] = {row, 64, n * row, halves * n * row};
+  const uint32_t box[5] = {64, box_rows, (uint32_t)c.cb, (uint32_t)halves, 1};
+  if (halves > 1) return few_map(m, base, 5, dims, strides, box);
+  const uint64_t d4[4] = {64, n, (uint64_t)c.blocks, E}, s4[3] = {row, 64, n * row};
+  const uint32_t b4[4] = {64, box_rows, (uint32_t)c.cb, 1};
+  return few_map(m, base, 4, d4, s4, b4);
+}
+
+// the same for the scales, [row][n][halves][E]
+bool few_scale_map(CUtensorMap* m, const void* base, uint64_t n, const FewChunks& c, uint64_t row, uint64_t halves,
+                   uint64_t E, uint32_t box_rows) {
+  const uint64_t d4[4] = {row, n, halves, E}, s4[3] = {row, n * row, halves * n * row};
+  const uint32_t b4[4] = {(uint32_t)c.sc, box_rows, (uint32_t)halves, 1};
+  if (halves > 1) return few_map(m, base, 4, d4, s4, b4);
+  const uint64_t d3[3] = {row, n, E}, s3[2] = {row, n * row};
+  const uint32_t b3[3] = {(uint32_t)c.sc, box_rows, 1};
+  return few_map(m, base, 3, d3, s3, b3);
+}
+
+}  // namespace
 
 cudaError_t launch_few_layer(const moe_shape& s, const Layout& L, char* ws, const uint16_t* x,
                              const moe_weights& w, const moe_w4_experts* q, float* out,
@@ -525,32 +1165,75 @@ cudaError_t launch_few_layer(const moe_shape& s, const Layout& L, char* ws, cons
   a.w_router = w.w_router;
   a.bias = w.router_bias;
   a.wsg = static_cast<const uint16_t*>(w.w_shared_gate);
-  a.gate_up = static_cast<const uint8_t*>(q ? q->q_gate_up : w.w_gate_up);
-  a.down = static_cast<const uint8_t*>(q ? q->q_down : w.w_down);
-  a.s_gate_up = q ? static_cast<const uint16_t*>(q->s_gate_up) : nullptr;
-  a.s_down = q ? static_cast<const uint16_t*>(q->s_down) : nullptr;
   a.shift = q ? (q->group == 32 ? 0 : q->group == 64 ? 1 : 2) : 0;
-  a.ws_gate_up = static_cast<const uint16_t*>(w.ws_gate_up);
-  a.ws_down = static_cast<const uint16_t*>(w.ws_down);
   a.out = out;
   a.ids = ids;
   a.w = topk_w;
   a.gap = gap;
   a.logits = reinterpret_cast<double*>(ws + L.logits);
   a.h = reinterpret_cast<uint16_t*>(ws + L.few_h);
-  a.h_plane = (size_t)s.T * (s.k + 1) * L.ldh;
   a.ldh = L.ldh;
+  a.ldl = (s.E + 2) / 2 * 2;
   a.sync = reinterpret_cast<uint32_t*>(ws + L.status) + kFewSyncWord;
   a.status = reinterpret_cast<uint32_t*>(ws + L.status);
   a.T = s.T; a.H = s.H; a.E = s.E; a.k = s.k; a.I = s.I; a.Is = s.Is;
-  const size_t smem = (sizeof(FewShared) + 127) / 128 * 128 + (size_t)s.T * (2 * s.H + 64);
-  const void* fn = q ? (const void*)few_layer_kernel<true> : (const void*)few_layer_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+
+  // rows of a pass: what the accumulators hold, and with scales for 128 weights what leaves room
+  // for eight blocks (16 bytes of their scales) in the smaller stage
+  const int cap = a.shift == 2 ? 28 : kFewRows;
+  const int most_rows = (s.H + sms - 1) / sms, passes = (most_rows + cap - 1) / cap;
+  a.rows = (most_rows + passes - 1) / passes;
+  // Eight stages, four where x leaves less room: a multiple of the teams, so that a slot of the
+  // ring always belongs to the same team. (A team that came to another's slot could find the
+  // barrier one phase behind, which looks like the phase it waits for.)
+  const int x_bytes = s.T * (2 * s.H + 64);
+  for (a.stages = 6;; a.stages -= kFewTeams) {
+    // the units of h take their size from the chunks, and the stages what they leave: settled in
+    // a few rounds from above
+    for (a.stage_bytes = 24576;; a.stage_bytes -= 1024) {
+      a.gu_s = few_chunks(s.H, 16, false, 0, a.stage_bytes, 32);
+      a.gu = few_chunks(s.H, 16, q != nullptr, a.shift, a.stage_bytes, 32);
+      // the limit keeps a unit of h near 6 KB
+      a.dn_s = few_chunks(s.Is, a.rows, false, 0, a.stage_bytes, 32);
+      a.dn = few_chunks(s.I, a.rows, q != nullptr, a.shift, a.stage_bytes, q ? 8 : 32);
+      // 64 mod 128 bytes (banks), more of them than one stage can need
+      a.unit = std::max(a.dn_s.cb * 192, a.dn.cb * (q ? 768 : 192)) | 64;
+      a.h_bytes = (std::max(x_bytes, (s.T + 4) * a.unit) + 127) / 128 * 128;
+      if (kFewSharedBytes + a.h_bytes + (size_t)a.stages * a.stage_bytes <= kFewSmem) break;
+      if (a.stage_bytes <= kFewMinStage) break;
+    }
+    a.units = std::min(a.h_bytes / a.unit, 64);
+    if (kFewSharedBytes + a.h_bytes + (size_t)a.stages * a.stage_bytes <= kFewSmem) break;
+    if (a.stages <= 4) return cudaErrorInvalidValue;
+  }
+
+  FewMaps m;
+  bool ok = few_weight_map(&m.gu_s, w.ws_gate_up, s.Is, a.gu_s, 2 * (uint64_t)s.H, 2, 1, 8) &&
+            few_weight_map(&m.dn_s, w.ws_down, s.H, a.dn_s, 2 * (uint64_t)s.Is, 1, 1, a.rows);
+  if (q) {
+    const uint64_t gr = w4_row_bytes(s.H), dr = w4_row_bytes(s.I);
+    const uint64_t gs = 2 * w4_row_scales(s.H, q->group), ds = 2 * w4_row_scales(s.I, q->group);
+    ok = ok && few_weight_map(&m.gu, q->q_gate_up, s.I, a.gu, gr, 2, s.E, 8) &&
+         few_weight_map(&m.dn, q->q_down, s.H, a.dn, dr, 1, s.E, a.rows) &&
+         few_scale_map(&m.gu_sc, q->s_gate_up, s.I, a.gu, gs, 2, s.E, 8) &&
+         few_scale_map(&m.dn_sc, q->s_down, s.H, a.dn, ds, 1, s.E, a.rows);
+  } else {
+    ok = ok && few_weight_map(&m.gu, w.w_gate_up, s.I, a.gu, 2 * (uint64_t)s.H, 2, s.E, 8) &&
+         few_weight_map(&m.dn, w.w_down, s.H, a.dn, 2 * (uint64_t)s.I, 1, s.E, a.rows);
+  }
+  if (!ok || 8 * s.T * a.ldl > a.stages * a.stage_bytes) return cudaErrorInvalidValue;
+
+  const size_t smem = kFewSharedBytes + a.h_bytes + (size_t)a.stages * a.stage_bytes;
+  const void* fn = !q ? (const void*)few_layer_kernel<-1>
+                   : a.shift == 0 ? (const void*)few_layer_kernel<0>
+                   : a.shift == 1 ? (const void*)few_layer_kernel<1>
+                                  : (const void*)few_layer_kernel<2>;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmem);
   if (e != cudaSuccess) return e;
   LaunchScope scope(MOE_K_OTHER, st);
-  void* params[] = {&a};
+  void* params[] = {&a, &m};
   // cooperative: the CTAs wait for one another, so all of them have to be resident at once
-  e = cudaLaunchCooperativeKernel(fn, dim3(sms), dim3(kFewThreads), params, smem, st);
+  e = cudaLaunchCooperativeKernel(fn, dim3(sms), dim3(kFewBlock), params, smem, st);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

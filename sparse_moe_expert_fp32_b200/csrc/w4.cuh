@@ -5,15 +5,14 @@
 // of its group. A row is stored in blocks of 128 elements = 64 bytes = 16 words; word
 // 4 t + j holds elements 32 j + 8 t + i (i < 8), element i in nibble (i >> 1) + 4 (i & 1).
 //
-// Why this order. The products run on mma.sync.m16n8k16 with the weights as A (16 weight
-// rows) and the tokens as B (8 tokens): a few tokens give each weight 8 columns of use at
-// most, so the kernels are bound by the weight bytes and take the tensor instruction only
-// for its cheap operand path; a tcgen05 tile would need the dequantised weights written back
-// to shared memory first. In an A fragment lane 4 g + t holds elements of row g at K
-// positions that depend on t alone, and the sum over K may run in any order. So lane t takes
-// its 16-byte quarter of a block in one load: word j is its share (8 of 32 elements) of the
-// j-th 32-element group, two whole MMAs of one scale group, and the nibble order makes
-// ((word >> 4 m) & 0x000f000f) the element pair (2 m, 2 m + 1) as it lies in a row of x.
+// Why this order. The products run on mma.sync.m16n8k16: a few tokens give each weight at most
+// 16 uses, so the kernels are bound by the weight bytes, and a tensor instruction is only the
+// cheapest way to spend them (a tcgen05 tile would need the dequantised weights written back to
+// shared memory, four times the codes' bytes). Its operands are register quads (A) and pairs (B)
+// that have to be consecutive, and a move costs as much as any other instruction, so both uses
+// below take them as they come out of one load. A thread reads 16 bytes of one weight row: lane
+// 4 g + t the quarter t of row g. Since a sum over K may run in any order, a word of codes, an
+// eighth of a 32-element part of one scale group, becomes four consecutive pairs of elements.
 #pragma once
 
 #include <stdint.h>
@@ -32,31 +31,70 @@ __host__ __device__ inline int64_t w4_row_scales(int64_t K, int group) {
   return ((K + group - 1) / group + 7) / 8 * 8;
 }
 
-// D += A B, m16n8k16, fp32 accumulators; A and B both bf16 or both fp16.
+// D = A B (+ D), m16n8k16, fp32 accumulators; A and B both bf16 or both fp16.
+#define MOE_MMA_16816(T) "mma.sync.aligned.m16n8k16.row.col.f32." T "." T ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   if constexpr (F16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
-        " {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm volatile(MOE_MMA_16816("f16") "{%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
-        " {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm volatile(MOE_MMA_16816("bf16") "{%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(MOE_MMA_16816("f16") "{%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile(MOE_MMA_16816("bf16") "{%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// The 32 elements x 16 rows of one K block of 32: lane 4 g + t holds 16 bytes of row g (a) and
-// of row g + 8 (b) at elements 8 t .. 8 t + 7, and of token g (x) at the same elements.
+// 8 weight rows by 32 elements as A. Lane 4 g + t holds elements 8 t .. 8 t + 7 of row g, four
+// registers in order, so MMA row g has the register pairs 0 and 2 and MMA row g + 8 the pairs 1 and 3
+// of the same weight row. B gives columns 0-3 the elements that belong to the first (`x`: registers 0
+// and 2 of a column's 16 bytes) and columns 4-7 those of the second (registers 1 and 3): four columns
+// of x, d[0], d[1] of lanes t < 2 and d[2], d[3] of lanes t >= 2 hold the two halves of their sums,
+// and the rest of D means nothing. See fold().
+template <bool FIRST>
+__device__ __forceinline__ void mma_rows(float (&d)[4], const uint4& w, const uint2& x) {
+  if constexpr (FIRST) mma16816_first<false>(d, w.x, w.y, w.z, w.w, x.x, x.y);
+  else mma16816<false>(d, w.x, w.y, w.z, w.w, x.x, x.y);
+}
+// Where the four words of a column's 16 bytes are kept for it: 0, 2, 1, 3.
+__host__ __device__ __forceinline__ int mma_rows_word(int i) { return (i & 1) * 2 + (i >> 1); }
+
+// 8 weight rows by 32 elements as B, 16 rows of x as A: two quads {x[g], x[g + 8]} x {registers 0, 1}
+// and x {registers 2, 3}. D: d[0], d[1]: row g of x, weight rows 2 t and 2 t + 1; d[2], d[3]: row g + 8.
 template <bool F16>
-__device__ __forceinline__ void mma_k32(float (&d)[4], const uint4& a, const uint4& b,
-                                        const uint4& x) {
-  mma16816<F16>(d, a.x, b.x, a.y, b.y, x.x, x.y);
-  mma16816<F16>(d, a.z, b.z, a.w, b.w, x.z, x.w);
+__device__ __forceinline__ void mma_cols(float (&d)[4], const uint4& x0, const uint4& x1, const uint4& w) {
+  mma16816_first<F16>(d, x0.x, x0.y, x0.z, x0.w, w.x, w.y);
+  mma16816<F16>(d, x1.x, x1.y, x1.z, x1.w, w.z, w.w);
+}
+
+// Shared memory by 32-bit address; lds_v2_if leaves v as it is where p is 0.
+__device__ __forceinline__ uint4 lds_v4(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint2 lds_v2(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void lds_v2_if(uint2& v, uint32_t at, int p) {
+  asm volatile("{\n .reg .pred q;\n setp.ne.s32 q, %3, 0;\n @q ld.shared.v2.u32 {%0,%1}, [%2];\n}\n"
+               : "+r"(v.x), "+r"(v.y)
+               : "r"(at), "r"(p));
 }
 
 __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
@@ -101,19 +139,31 @@ __device__ __forceinline__ uint4 w4_pairs(uint32_t w) {
   return r;
 }
 
-// The scales of a block's four 32-element parts: group 32 << shift elements, `s` the row.
-__device__ __forceinline__ void w4_block_scales(const uint16_t* s, int block, int shift, float (&f)[4]) {
-  if (shift == 0) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(s + 4 * (int64_t)block));
-    f[0] = bf16lo(v.x); f[1] = bf16hi(v.x);
-    f[2] = bf16lo(v.y); f[3] = bf16hi(v.y);
-  } else if (shift == 1) {
-    const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(s + 2 * (int64_t)block));
-    f[0] = f[1] = bf16lo(v);
-    f[2] = f[3] = bf16hi(v);
-  } else {
-    f[0] = f[1] = f[2] = f[3] = bf16lo(__ldg(s + block));
+// The scales of a block's four 32-element parts as four bf16: group 32 << shift elements, `s` the
+// row's scales in global memory, `at` their address in shared memory.
+__device__ __forceinline__ uint2 w4_spread1(uint32_t v) {
+  return make_uint2(__byte_perm(v, v, 0x1010), __byte_perm(v, v, 0x3232));
+}
+__device__ __forceinline__ uint2 w4_block_scales(const uint16_t* s, int block, int shift) {
+  if (shift == 0) return __ldg(reinterpret_cast<const uint2*>(s + 4 * (int64_t)block));
+  if (shift == 1) return w4_spread1(__ldg(reinterpret_cast<const uint32_t*>(s + 2 * (int64_t)block)));
+  const uint32_t v = __ldg(s + block) * 0x10001u;
+  return make_uint2(v, v);
+}
+template <int SHIFT>
+__device__ __forceinline__ uint2 w4_block_scales(uint32_t at, int block) {
+  uint32_t v;
+  if constexpr (SHIFT == 0) return lds_v2(at + 8 * block);
+  if constexpr (SHIFT == 1) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at + 4 * block));
+    return w4_spread1(v);
   }
+  asm volatile("{\n .reg .u16 h;\n ld.shared.u16 h, [%1];\n mov.b32 %0, {h, h};\n}\n" : "=r"(v) : "r"(at + 2 * block));
+  return make_uint2(v, v);
+}
+__device__ __forceinline__ float w4_scale(const uint2& s, int j) {
+  const uint32_t v = j & 2 ? s.y : s.x;
+  return j & 1 ? bf16hi(v) : bf16lo(v);
 }
 
 }  // namespace moe

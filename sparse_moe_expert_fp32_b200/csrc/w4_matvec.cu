@@ -3,7 +3,7 @@
 //   y[t, n] = sum_k x[t, k] (c[n, k] - 8) s[n, k / group]
 //
 // Bound by the weight bytes, 1/2 + 2/group each. CTA b of the grid owns the matrix rows
-// [b N / grid, (b + 1) N / grid) and takes them 32 at a time (two m16 tiles); its 16 warps
+// [b N / grid, (b + 1) N / grid) and takes them 32 at a time (four tiles of 8); its 16 warps
 // split the row's 128-element blocks, so a CTA has no partner to wait for and small matrices
 // still spread over all SMs. x is staged in shared memory once per K chunk. The codes enter
 // the MMA as exact integers, a 32-element part at a time; its fp32 sum is multiplied by the
@@ -60,56 +60,43 @@ matvec_w4_kernel(const MvArgs a) {
     __syncthreads();
     for (int64_t r0 = n0; r0 < n1; r0 += kMvRows) {
       const int nr = (int)min((int64_t)kMvRows, n1 - r0);
-      float acc[2][NT][4] = {};
+      float acc[4][4] = {};
       for (int b = warp; b < nb; b += kMvWarps) {
         const int64_t kb = k0 / kW4Block + b;
         uint4 q[4];
-        float sc[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // rows g, g + 8, g + 16, g + 24
-          q[i] = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
-          sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
-          if (g + 8 * i < nr) {
-            const int64_t n = r0 + g + 8 * i;
-            q[i] = ld_stream_v4(a.q + n * a.row_bytes + kb * kW4BlockBytes + 16 * t4);
-            w4_block_scales(a.s + n * a.row_scales, (int)kb, a.shift, sc[i]);
-          }
-        }
+        for (int i = 0; i < 4; ++i)
+          q[i] = ld_stream_v4(a.q + (r0 + min(g + 8 * i, nr - 1)) * a.row_bytes + kb * kW4BlockBytes + 16 * t4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint4 xb[NT];
+        for (int i = 0; i < 4; ++i) {
+          if (8 * i >= nr) break;
+          const uint2 s0 = w4_block_scales(a.s + (r0 + min(8 * i + 2 * t4, nr - 1)) * a.row_scales, (int)kb, a.shift);
+          const uint2 s1 = w4_block_scales(a.s + (r0 + min(8 * i + 2 * t4 + 1, nr - 1)) * a.row_scales, (int)kb, a.shift);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            xb[nt] = make_uint4(0u, 0u, 0u, 0u);
-            if (nt * 8 + g < a.T)
-              xb[nt] = *reinterpret_cast<const uint4*>(xs + (size_t)(nt * 8 + g) * pitch + b * 256 +
-                                                       64 * j + 16 * t4);
-          }
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const uint32_t wa = (&q[2 * m].x)[j], wb = (&q[2 * m + 1].x)[j];
-            const uint4 pa = w4_pairs<F16>(wa), pb = w4_pairs<F16>(wb);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float d[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_k32<F16>(d, pa, pb, xb[nt]);
-              acc[m][nt][0] = fmaf(d[0], sc[2 * m][j], acc[m][nt][0]);
-              acc[m][nt][1] = fmaf(d[1], sc[2 * m][j], acc[m][nt][1]);
-              acc[m][nt][2] = fmaf(d[2], sc[2 * m + 1][j], acc[m][nt][2]);
-              acc[m][nt][3] = fmaf(d[3], sc[2 * m + 1][j], acc[m][nt][3]);
-            }
+          for (int j = 0; j < 4; ++j) {
+            const uint8_t* xp = xs + (size_t)g * pitch + b * 256 + 64 * j + 16 * t4;
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            const uint4 x0 = g < a.T ? *reinterpret_cast<const uint4*>(xp) : zero;
+            const uint4 x1 = g + 8 < a.T ? *reinterpret_cast<const uint4*>(xp + 8 * (size_t)pitch) : zero;
+            float d[4];
+            mma_cols<F16>(d, make_uint4(x0.x, x1.x, x0.y, x1.y), make_uint4(x0.z, x1.z, x0.w, x1.w),
+                          w4_pairs<F16>((&q[i].x)[j]));
+            acc[i][0] = fmaf(d[0], w4_scale(s0, j), acc[i][0]);
+            acc[i][1] = fmaf(d[1], w4_scale(s1, j), acc[i][1]);
+            acc[i][2] = fmaf(d[2], w4_scale(s0, j), acc[i][2]);
+            acc[i][3] = fmaf(d[3], w4_scale(s1, j), acc[i][3]);
           }
         }
       }
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float2*>(red + ((size_t)warp * kMvRows + 16 * m + 8 * h + g) * (NT * 8) +
-                                       8 * nt + 2 * t4) =
-                make_float2(acc[m][nt][2 * h], acc[m][nt][2 * h + 1]);
+        for (int h = 0; h < 2; ++h)
+          if (h == 0 || NT == 2) {
+            float* at = red + ((size_t)warp * kMvRows + 8 * i + 2 * t4) * (NT * 8) + 8 * h + g;
+            at[0] = acc[i][2 * h];
+            at[NT * 8] = acc[i][2 * h + 1];
+          }
       __syncthreads();
       for (int o = tid; o < kMvRows * NT * 8; o += kMvThreads) {
         const int r = o % kMvRows, t = o / kMvRows;
