@@ -33,23 +33,23 @@
 namespace moe {
 namespace {
 
-constexpr int kFewWarps = 8;     // consumers
+constexpr int kFewWarps = 12;    // consumers
 constexpr int kFewThreads = kFewWarps * 32;
 constexpr int kFewTeam = 4;      // warps that share a stage; the stages go to the teams in turn
 constexpr int kFewTeams = kFewWarps / kFewTeam;
 constexpr int kFewBlock = kFewThreads + 2 * 32;  // and one warp that feeds them weights, one h
 constexpr int kFewPairs = kFewMaxT * (kMaxK + 1);  // (token, expert) pairs, shared expert included
 constexpr int kFewRows = 32;                       // output rows of one pass of the down stage
-constexpr int kFewMaxStages = 8;
-constexpr int kFewMinStage = 15360;  // holds 28 rows of eight blocks with scales, 32 rows of five (few_chunks)
+constexpr int kFewMaxStages = 16;
 constexpr uint64_t kFewWaitNs = 2000000000ull;
 constexpr uint64_t kFewDrainNs = 200000000ull;
-constexpr int kBarConsumers = 1, kBarRouted = 2;   // named barriers
+constexpr int kBarConsumers = 1, kBarRouted = 2, kBarTeam = 3;  // named barriers
 
 // How a weight matrix comes through the ring: `n` chunks of a row, `cb` 64-byte blocks each (a block
 // is 32 bf16 or 128 4-bit weights); scales `sc` bytes of a row and chunk.
 struct FewChunks {
   int n, cb, sc, blocks;
+  __device__ int scale_at(int c, int shift) const { return c * cb * 8 >> shift; }  // bytes, of chunk c
 };
 
 struct FewArgs {
@@ -69,6 +69,7 @@ struct FewArgs {
   FewChunks gu, gu_s, dn, dn_s;  // gate|up and down matrices, routed and shared
   int rows;                      // output rows of a pass
   int stages, stage_bytes;
+  int group, slot;               // experts of a down stage at most, bytes of one of them in it
   int unit, units, h_bytes;      // ring of h: bytes of a token's chunk, number of them, region
 };
 
@@ -82,6 +83,7 @@ struct FewMaps {
 
 struct FewShared {
   uint64_t full[kFewMaxStages], empty[kFewMaxStages], x_full, logits_full;
+  int tag[kFewMaxStages];                   // number of the stage that a slot is filled with
   uint8_t stage_units[kFewMaxStages];       // units of h that a stage in flight uses
   union {
     double part[2 * kFewWarps * 16 * kFewMaxT / 2];  // router partial sums: [stage][warp of the team][token]
@@ -89,7 +91,8 @@ struct FewShared {
       uint64_t key[kFewMaxT][64];            // selection: candidates of a token
       uint16_t e[kFewMaxT][64];
     } cand;
-    float red[2][kFewWarps][16 * kFewMaxT];  // cross-warp sums; the down stage uses both halves
+    float red[2][kFewTeams][kFewTeam][16 * kFewMaxT];  // cross-warp sums of the teams' tiles
+    float out[kFewWarps][kFewRows][kFewMaxT];          // and of the down stage
   };
   uint32_t mask[kMaxE];                     // tokens that chose an expert
   uint16_t index[kMaxE];                    // its place among the active ones
@@ -105,7 +108,7 @@ struct FewShared {
   int n_act;
   int aborted;
 };
-static_assert(2 * 16 * kFewMaxT == kFewRows * kFewMaxT, "the two users of FewShared::red");
+
 
 constexpr size_t kFewSharedBytes = (sizeof(FewShared) + 127) / 128 * 128;
 constexpr size_t kFewSmem = 227 * 1024;
@@ -184,19 +187,38 @@ struct Cursor {
   }
 };
 
-// A consumer's place: the number of the stage its team takes next, and the ring's slot for it.
+// A consumer's place: the number of a stage and the ring's slot for it.
 struct Place {
   int i;
   Cursor cur;
-  __device__ void next(int stages) {
-    i += kFewTeams;
-    cur.s += kFewTeams;
-    while (cur.s >= stages) {
-      cur.s -= stages;
-      cur.parity ^= 1u;
-    }
+  __device__ void skip(int n, int stages) {
+    i += n;
+    for (cur.s += n; cur.s >= stages; cur.s -= stages) cur.parity ^= 1u;
   }
 };
+
+// Wait for the stage at `at`. A slot's stages go to different teams, and a team may come to it while
+// the stage before is still on its way, one phase behind: that looks like the phase it waits for.
+// So the slot also says which stage it is being filled with (it is not before the last one has been
+// used up).
+__device__ __noinline__ void tag_slow(volatile int* tag, int i, FewShared& S, uint32_t* status) {
+  uint64_t t0 = 0;
+  for (uint32_t spin = 1; *tag != i; ++spin)
+    if ((spin & 255u) == 0) {
+      if (*reinterpret_cast<volatile int*>(&S.aborted)) return;
+      const uint64_t t = globaltimer_ns();
+      if (!t0) t0 = t;
+      if (t - t0 > kFewWaitNs) {
+        give_up(S, status);
+        return;
+      }
+    }
+}
+__device__ __forceinline__ void wait_stage(const Place& at, FewShared& S, uint32_t* status) {
+  volatile int* tag = &S.tag[at.cur.s];
+  if (*tag != at.i) tag_slow(tag, at.i, S, status);
+  wait_phase(&S.full[at.cur.s], at.cur.parity, S, status);
+}
 
 __device__ __forceinline__ int round128(int v) { return (v + 127) & ~127; }
 
@@ -234,20 +256,21 @@ struct Feeder {
   FewShared& S;
   uint8_t* ring;
   Cursor cur;
-  int issued;  // stages filled so far, up to the ring's size
+  int count;  // stages filled so far
   bool ok;
 
   __device__ uint8_t* begin() {
     ok = ok && wait_phase(&S.empty[cur.s], cur.parity ^ 1u, S, a.status);
     return ring + (size_t)cur.s * a.stage_bytes;
   }
+  __device__ void tag() { *const_cast<volatile int*>(&S.tag[cur.s]) = count; }  // before the arrival
   __device__ void end() {
     cur.next(a.stages);
-    if (issued < a.stages) ++issued;
+    ++count;
   }
   // leave no copy in flight: wait for the last phase of every stage that was filled
   __device__ void drain() {
-    for (int i = 0; i < issued; ++i) {
+    for (int i = 0; i < min(count, a.stages); ++i) {
       cur.s = cur.s ? cur.s - 1 : a.stages - 1;
       if (cur.s == a.stages - 1) cur.parity ^= 1u;
       uint64_t t0 = 0;
@@ -461,85 +484,100 @@ __device__ void feed_gate_up(Feeder& f, const FewMaps& m, bool h, Tiles& tile, i
       if (h) {
         ptx::mbar_arrive(bar);
       } else {
+        f.tag();
         ptx::mbar_arrive_expect_tx(bar, 1024 * ch.cb + (w4 ? 16 * ch.sc : 0));
         tma_5d(dst, shared ? &m.gu_s : &m.gu, bar, 0, c0, c * ch.cb, 0, e);
-        if (w4) tma_4d(dst + 1024 * ch.cb, &m.gu_sc, bar, c * ch.sc, c0, 0, e);
+        if (w4) tma_4d(dst + 1024 * ch.cb, &m.gu_sc, bar, ch.scale_at(c, a.shift) & ~15, c0, 0, e);
       }
       f.end();
     }
   }
 }
 
-// This team's chunks of the tile whose first stage is `first`: this warp's blocks of the gate and the
-// up rows, for 4 NQ tokens. xg: x of the lane's first column, rows of 16-byte words in the order
-// of mma_rows_word. An MMA chain is a stage's blocks at most; stages add up in fp32.
-template <int FMT, int NQ>
-__device__ __forceinline__ void tile_sums(const FewArgs& a, FewShared& S, const FewChunks& ch, uint32_t ring,
-                                          Place& at, int first, uint32_t xg, int xstep, const int (&tok)[NQ],
-                                          int warp, int lane, float (&gate)[NQ][4], float (&up)[NQ][4]) {
+// The chunks of one tile, by one team: this warp's blocks of the gate and the up rows. bf16 weights
+// are the MMA's A by mma_rows, 8 rows at a time, for 4 NQ tokens: `low` says which half of a
+// column's registers the lane gives. An MMA chain is a stage's blocks at most; stages add up in fp32.
+template <int NQ>
+__device__ __forceinline__ void tile_bf16(const FewArgs& a, FewShared& S, const FewChunks& ch, uint32_t ring,
+                                          Place at, uint32_t xs, int xpitch, int warp, int lane,
+                                          float (&gate)[NQ][4], float (&up)[NQ][4]) {
   const int g = lane >> 2, t4 = lane & 3, wt = warp & (kFewTeam - 1);
-  uint2 x[NQ];  // stays zero in the lanes of no token
+  const bool low = g < 4;
+  const uint32_t xg = xs + (g & 3) * xpitch + 16 * t4;
+  int tok[NQ];
 #pragma unroll
-  for (int q = 0; q < NQ; ++q) x[q] = make_uint2(0u, 0u);
-  for (; at.i < first + ch.n; at.next(a.stages)) {
+  for (int q = 0; q < NQ; ++q) tok[q] = 4 * q + (g & 3) < a.T;
+  uint4 x[NQ];  // stays zero in the lanes of no token
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) x[q] = make_uint4(0u, 0u, 0u, 0u);
+  for (int c = 0; c < ch.n; ++c, at.skip(1, a.stages)) {
     const uint32_t st = ring + at.cur.s * a.stage_bytes;
-    const int b0 = (at.i - first) * ch.cb, nb = min(ch.cb, ch.blocks - b0);
-    wait_phase(&S.full[at.cur.s], at.cur.parity, S, a.status);
-    uint32_t wp = st + 64 * g + 16 * t4 + 512 * wt;
+    const int b0 = c * ch.cb, nb = min(ch.cb, ch.blocks - b0);
+    wait_stage(at, S, a.status);
+    uint32_t wp = st + 64 * g + 16 * t4 + 512 * wt, xp = xg + (b0 + wt) * 64;
     const uint32_t up_at = 512 * ch.cb;
-    if constexpr (FMT >= 0) {
-      uint32_t xp = xg + (b0 + wt) * 256;
-      const uint32_t sp = st + 1024 * ch.cb + g * ch.sc;
-      for (int b = wt; b < nb; b += kFewTeam, wp += 512 * kFewTeam, xp += 256 * kFewTeam) {
-        const uint4 wg = lds_v4(wp), wu = lds_v4(wp + up_at);
-        const uint2 sg = w4_block_scales<FMT>(sp, b), su = w4_block_scales<FMT>(sp + 8 * ch.sc, b);
-        const int parts = min(4, a.H / 32 - 4 * (b0 + b));
-        float dg[NQ][4], du[NQ][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j >= 2 && j >= parts) break;  // H is a multiple of 64: two parts or four
-          const uint4 pg = w4_pairs<false>((&wg.x)[j]), pu = w4_pairs<false>((&wu.x)[j]);
-#pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            lds_v2_if(x[q], xp + q * xstep + 64 * j, tok[q]);
-            // the parts of a group share a chain and a scale
-            if (j % (1 << FMT) == 0) {
-              mma_rows<true>(dg[q], pg, x[q]);
-              mma_rows<true>(du[q], pu, x[q]);
-            } else {
-              mma_rows<false>(dg[q], pg, x[q]);
-              mma_rows<false>(du[q], pu, x[q]);
-            }
-            if ((j + 1) % (1 << FMT) == 0 || (j == 1 && parts == 2)) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                gate[q][i] = fmaf(dg[q][i], w4_scale(sg, j), gate[q][i]);
-                up[q][i] = fmaf(du[q][i], w4_scale(su, j), up[q][i]);
-              }
-            }
-          }
-        }
-      }
-    } else {
-      uint32_t xp = xg + (b0 + wt) * 64;
-      float dg[NQ][4] = {}, du[NQ][4] = {};
+    float dg[NQ][4] = {}, du[NQ][4] = {};
 #pragma unroll 5
-      for (int b = wt; b < nb; b += kFewTeam, wp += 512 * kFewTeam, xp += 64 * kFewTeam) {
-        const uint4 wg = lds_v4(wp), wu = lds_v4(wp + up_at);
+    for (int b = wt; b < nb; b += kFewTeam, wp += 512 * kFewTeam, xp += 64 * kFewTeam) {
+      const uint4 wg = lds_v4(wp), wu = lds_v4(wp + up_at);
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          lds_v2_if(x[q], xp + q * xstep, tok[q]);
-          mma_rows<false>(dg[q], wg, x[q]);
-          mma_rows<false>(du[q], wu, x[q]);
+      for (int q = 0; q < NQ; ++q) {
+        lds_v4_if(x[q], xp + 4 * q * xpitch, tok[q]);
+        const uint2 y = make_uint2(low ? x[q].x : x[q].y, low ? x[q].z : x[q].w);
+        mma_rows<false>(dg[q], wg, y);
+        mma_rows<false>(du[q], wu, y);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        gate[q][i] += dg[q][i];
+        up[q][i] += du[q][i];
+      }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&S.empty[at.cur.s]);
+  }
+}
+
+// The same for 4-bit weights. Their operands come out of arithmetic and can go to any register, so
+// the MMA's A is the 8 gate rows and the 8 up rows, and its columns are the tokens. Chunks c, c + step, ...
+// acc[0], [1]: gate row g, tokens 2 t and 2 t + 1; acc[2], [3]: the up row.
+template <int FMT>
+__device__ __forceinline__ void tile_w4(const FewArgs& a, FewShared& S, const FewChunks& ch, uint32_t ring,
+                                        Place at, int c, int step, uint32_t xs, int xpitch, int warp, int lane,
+                                        float (&acc)[4]) {
+  const int g = lane >> 2, t4 = lane & 3, wt = warp & (kFewTeam - 1), tok = g < a.T;
+  const uint32_t xg = xs + g * xpitch + 16 * t4;
+  uint4 x = make_uint4(0u, 0u, 0u, 0u);  // stays zero in the lanes of no token
+  for (at.skip(c, a.stages); c < ch.n; c += step, at.skip(step, a.stages)) {
+    const uint32_t st = ring + at.cur.s * a.stage_bytes;
+    const int b0 = c * ch.cb, nb = min(ch.cb, ch.blocks - b0);
+    wait_stage(at, S, a.status);
+    uint32_t wp = st + 64 * g + 16 * t4 + 512 * wt, xp = xg + (b0 + wt) * 256;
+    const uint32_t up_at = 512 * ch.cb, sp = st + 1024 * ch.cb + g * ch.sc + (ch.scale_at(c, FMT) & 15);
+    for (int b = wt; b < nb; b += kFewTeam, wp += 512 * kFewTeam, xp += 256 * kFewTeam) {
+      const uint4 wg = lds_v4(wp), wu = lds_v4(wp + up_at);
+      const uint2 sg = w4_block_scales<FMT>(sp, b), su = w4_block_scales<FMT>(sp + 8 * ch.sc, b);
+      const int parts = min(4, a.H / 32 - 4 * (b0 + b));
+      float d[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j >= 2 && j >= parts) break;  // H is a multiple of 64: two parts or four
+        const uint4 pg = w4_pairs<false>(word(wg, j)), pu = w4_pairs<false>(word(wu, j));
+        lds_v4_if(x, xp + 64 * j, tok);
+        // the parts of a group share a chain and a scale
+        if (j % (1 << FMT) == 0) mma16816_first<false>(d, pg.x, pu.x, pg.y, pu.y, x.x, x.y);
+        else mma16816<false>(d, pg.x, pu.x, pg.y, pu.y, x.x, x.y);
+        mma16816<false>(d, pg.z, pu.z, pg.w, pu.w, x.z, x.w);
+        if ((j + 1) % (1 << FMT) == 0 || (j == 1 && parts == 2)) {
+          const float fg = w4_scale(sg, j), fu = w4_scale(su, j);
+          acc[0] = fmaf(d[0], fg, acc[0]);
+          acc[1] = fmaf(d[1], fg, acc[1]);
+          acc[2] = fmaf(d[2], fu, acc[2]);
+          acc[3] = fmaf(d[3], fu, acc[3]);
         }
       }
-#pragma unroll
-      for (int q = 0; q < NQ; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          gate[q][i] += dg[q][i];
-          up[q][i] += du[q][i];
-        }
     }
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&S.empty[at.cur.s]);
@@ -555,73 +593,77 @@ __device__ __forceinline__ void fold(const float (&d)[4], bool low, float& v0, f
   v1 += __shfl_xor_sync(0xffffffffu, v1, 2);
 }
 
-// `stage`: the number of the first tile's first stage, on return that behind the last.
+// Tiles up to tile `end`; the teams take them in turn. `at`: the first tile's first stage, on return
+// the one behind the last tile's.
 template <int FMT, int NQ>
 __device__ __forceinline__ void gate_up_tiles(const FewArgs& a, FewShared& S, uint32_t xs, int xpitch,
-                                              uint32_t ring, Place& at, int& stage, Tiles& tile, int end) {
+                                              uint32_t ring, Place& at, Tiles& tile, int& turn, int end) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-  int tok[NQ];
-#pragma unroll
-  for (int q = 0; q < NQ; ++q) tok[q] = 4 * q + (g & 3) < a.T;
-  const uint32_t xg = xs + (g & 3) * xpitch + 16 * t4 + 8 * (g >> 2);
-  int buf = 0, turn = 0;
+  const int team = warp / kFewTeam, wt = warp & (kFewTeam - 1);
+  int buf = 0;
   for (; tile.u < end; tile.next()) {
     tile.settle(a.Is / 8, a.I / 8);
-    float gate[NQ][4] = {}, up[NQ][4] = {};
     const int s = tile.s, c0 = 8 * tile.c;
-    if (s == 0) {
-      tile_sums<-1, NQ>(a, S, a.gu_s, ring, at, stage, xg, 4 * xpitch, tok, warp, lane, gate, up);
-      stage += a.gu_s.n;
-    } else {
-      tile_sums<FMT, NQ>(a, S, a.gu, ring, at, stage, xg, 4 * xpitch, tok, warp, lane, gate, up);
-      stage += a.gu.n;
-    }
-    float* red = S.red[buf][warp];  // [gate, up][token][channel]
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      float g0, g1, v0, v1;
-      fold(gate[q], t4 < 2, g0, g1);
-      fold(up[q], t4 < 2, v0, v1);
-      float* to = red + 8 * (4 * q + 2 * (t4 & 1)) + g;
-      if (t4 < 2) {
-        to[0] = g0;
-        to[8] = g1;
+    const int n = s ? a.gu.n : a.gu_s.n;
+    // a tile with so many chunks that two of them do not fit in the ring is taken by both teams
+    const bool whole = FMT >= 0 && s && 2 * n > a.stages, mine = whole || turn == team;
+    if (!whole) turn = turn + 1 == kFewTeams ? 0 : turn + 1;
+    if (mine) {
+      float* red = S.red[buf][team][wt];  // [gate, up][token][channel]
+      if (FMT >= 0 && s) {
+        float acc[4] = {};
+        tile_w4<FMT < 0 ? 0 : FMT>(a, S, a.gu, ring, at, whole ? team : 0, whole ? kFewTeams : 1, xs, xpitch, warp,
+                                   lane, acc);
+        float* to = red + 16 * t4 + g;
+        to[0] = acc[0];
+        to[8] = acc[1];
+        to[64] = acc[2];
+        to[72] = acc[3];
       } else {
-        to[64] = v0;
-        to[72] = v1;
-      }
-    }
-    sync_consumers();
-    if (warp >> 1 == turn) {  // a pair of warps finishes the tile, another pair the next one
-      const int at64 = tid & 63, t = at64 >> 3, c = at64 & 7;
-      const uint32_t m = s ? S.act_mask[s] : (1u << a.T) - 1u;
-      if ((m >> t) & 1u) {
-        float gate = 0.f, up = 0.f;
+        float gate[NQ][4] = {}, up[NQ][4] = {};
+        tile_bf16<NQ>(a, S, s ? a.gu : a.gu_s, ring, at, xs, xpitch, warp, lane, gate, up);
 #pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) {
-          gate += S.red[buf][w][at64];
-          up += S.red[buf][w][64 + at64];
+        for (int q = 0; q < NQ; ++q) {
+          float g0, g1, v0, v1;
+          fold(gate[q], t4 < 2, g0, g1);
+          fold(up[q], t4 < 2, v0, v1);
+          float* to = red + 8 * (4 * q + 2 * (t4 & 1)) + g + (t4 < 2 ? 0 : 64);
+          to[0] = t4 < 2 ? g0 : v0;
+          to[8] = t4 < 2 ? g1 : v1;
         }
-        const int pair = s ? S.act_pair[s] + __popc(m & ((1u << t) - 1u)) : t;
-        const float h = gate / (1.f + expf(-gate)) * up * (s ? S.pair_w[pair] : 1.f);
-        // three truncated pieces: 8 + 8 + 8 significant bits, h exactly (an infinity or NaN in
-        // the first alone)
-        const uint32_t hb = __float_as_uint(h);
-        const bool fin = fabsf(h) <= FLT_MAX;
-        const float r1 = fin ? h - __uint_as_float(hb & 0xffff0000u) : 0.f;
-        const uint32_t mb = __float_as_uint(r1);
-        const float r2 = r1 - __uint_as_float(mb & 0xffff0000u);
-        const int ch = c0 + c;
-        uint16_t* o = a.h + ((size_t)pair * (a.ldh / 32) + ch / 32) * 96 + (ch % 32 & ~7) +
-                      2 * mma_rows_word(ch % 8 / 2) + ch % 2;
-        o[0] = (h == h) ? (uint16_t)(hb >> 16) : (uint16_t)0x7fc0u;
-        o[32] = (uint16_t)(mb >> 16);
-        o[64] = (uint16_t)(__float_as_uint(r2) >> 16);
-        asm volatile("fence.proxy.async.global;" ::: "memory");  // h is read by bulk copies
       }
+      if (whole) sync_consumers();
+      else ptx::bar_sync(kBarTeam + team, 32 * kFewTeam);
+      if (wt >> 1 == buf && (!whole || team == 0)) {  // a pair of the team's warps finishes the tile, the other pair its next one
+        const int at64 = tid & 63, t = at64 >> 3, c = at64 & 7;
+        const uint32_t m = s ? S.act_mask[s] : (1u << a.T) - 1u;
+        if ((m >> t) & 1u) {
+          float gate = 0.f, up = 0.f;
+          for (int q = whole ? 0 : team; q < (whole ? kFewTeams : team + 1); ++q)
+#pragma unroll
+            for (int w = 0; w < kFewTeam; ++w) {
+              gate += S.red[buf][q][w][at64];
+              up += S.red[buf][q][w][64 + at64];
+            }
+          const int pair = s ? S.act_pair[s] + __popc(m & ((1u << t) - 1u)) : t;
+          const float h = __fdividef(gate * up * (s ? S.pair_w[pair] : 1.f), 1.f + expf(-gate));
+          // three truncated pieces: 8 + 8 + 8 significant bits, h exactly (an infinity or NaN in
+          // the first alone)
+          const uint32_t hb = __float_as_uint(h);
+          const bool fin = fabsf(h) <= FLT_MAX;
+          const float r1 = fin ? h - __uint_as_float(hb & 0xffff0000u) : 0.f;
+          const uint32_t mb = __float_as_uint(r1);
+          const float r2 = r1 - __uint_as_float(mb & 0xffff0000u);
+          const int ch = c0 + c;
+          uint16_t* o = a.h + ((size_t)pair * (a.ldh / 32) + ch / 32) * 96 + ch % 32;
+          o[0] = (h == h) ? (uint16_t)(hb >> 16) : (uint16_t)0x7fc0u;
+          o[32] = (uint16_t)(mb >> 16);
+          o[64] = (uint16_t)(__float_as_uint(r2) >> 16);
+        }
+      }
+      buf ^= 1;  // the team's next tile uses the other half: one barrier a tile is enough
     }
-    buf ^= 1;  // the next tile's sums go to the other half: one barrier a tile is enough
-    turn = turn + 1 == kFewWarps / 2 ? 0 : turn + 1;
+    at.skip(n, a.stages);
   }
 }
 
@@ -629,25 +671,55 @@ __device__ __forceinline__ void gate_up_tiles(const FewArgs& a, FewShared& S, ui
 // CTA b owns the output rows [b H / grid, (b + 1) H / grid), a.rows (at most 32) in a pass.
 __device__ __forceinline__ int row_begin(const FewArgs& a, int b) { return (int)((int64_t)b * a.H / gridDim.x); }
 
+// Small experts come several to a stage: the active ones [s, s + n), n at most a.group, with `tokens`
+// (at most the units of h there are) between them.
+struct Group {
+  int n, tokens;
+};
+__device__ __forceinline__ Group group_at(const FewArgs& a, const FewShared& S, int s) {
+  Group g{1, __popc(S.act_mask[s])};
+  while (g.n < a.group && s + g.n < S.n_act) {
+    const int t = __popc(S.act_mask[s + g.n]);
+    if (g.tokens + t > a.units) break;
+    g.tokens += t;
+    ++g.n;
+  }
+  return g;
+}
+
 template <int FMT>
 __device__ void feed_down(Feeder& f, const FewMaps& m) {
   const FewArgs& a = f.a;
   const int n1 = row_begin(a, blockIdx.x + 1);
-  for (int r0 = row_begin(a, blockIdx.x); r0 < n1; r0 += a.rows)
-    for (int s = 0; s < f.S.n_act; ++s) {
-      const FewChunks& ch = s ? a.dn : a.dn_s;
-      const int e = s ? f.S.act_e[s] : 0, bytes = a.rows * 64 * ch.cb;
-      for (int c = 0; c < ch.n; ++c) {
+  for (int r0 = row_begin(a, blockIdx.x); r0 < n1; r0 += a.rows) {
+    const int shared = a.rows * 64 * a.dn_s.cb, routed = a.rows * 64 * a.dn.cb, scales = FMT >= 0 ? a.rows * a.dn.sc : 0;
+    for (int c = 0; c < a.dn_s.n; ++c) {
+      uint8_t* dst = f.begin();
+      if (!f.ok) return;
+      uint64_t* bar = &f.S.full[f.cur.s];
+      f.tag();
+      ptx::mbar_arrive_expect_tx(bar, shared);
+      tma_4d(dst, &m.dn_s, bar, 0, r0, c * a.dn_s.cb, 0);
+      f.end();
+    }
+    for (int s = 1; s < f.S.n_act;) {
+      const Group g = group_at(a, f.S, s);
+      for (int c = 0; c < a.dn.n; ++c) {
         uint8_t* dst = f.begin();
         if (!f.ok) return;
         uint64_t* bar = &f.S.full[f.cur.s];
-        const bool w4 = FMT >= 0 && s;
-        ptx::mbar_arrive_expect_tx(bar, bytes + (w4 ? a.rows * ch.sc : 0));
-        tma_4d(dst, s ? &m.dn : &m.dn_s, bar, 0, r0, c * ch.cb, e);
-        if (w4) tma_3d(dst + round128(bytes), &m.dn_sc, bar, c * ch.sc, r0, e);
+        f.tag();
+        ptx::mbar_arrive_expect_tx(bar, g.n * (routed + scales));
+        for (int j = 0; j < g.n; ++j, dst += a.slot) {
+          const int e = f.S.act_e[s + j];
+          tma_4d(dst, &m.dn, bar, 0, r0, c * a.dn.cb, e);
+          if (FMT >= 0) tma_3d(dst + round128(routed), &m.dn_sc, bar, a.dn.scale_at(c, a.shift) & ~15, r0, e);
+        }
         f.end();
       }
+      s += g.n;
     }
+  }
 }
 
 // h for the same stages, once all of it is there.
@@ -666,199 +738,240 @@ __device__ void feed_h(Feeder& f, uint8_t* units) {
     --flight;
   };
   for (int r0 = row_begin(a, blockIdx.x); r0 < n1; r0 += a.rows)
-    for (int s = 0; s < S.n_act; ++s) {
+    for (int s = 0; s < S.n_act;) {
       const FewChunks& ch = s ? a.dn : a.dn_s;
-      const int nt = s ? __popc(S.act_mask[s]) : a.T;
+      const Group g = s ? group_at(a, S, s) : Group{1, a.T};
       const int block = FMT >= 0 && s ? 768 : 192, total = 6 * (s ? a.I : a.Is);
+      // the group's pairs follow one another
       const uint8_t* src = reinterpret_cast<const uint8_t*>(a.h) + (s ? (size_t)S.act_pair[s] : 0) * a.ldh * 6;
       for (int c = 0; c < ch.n; ++c) {
         f.begin();
         if (f.ok && flight == a.stages) pop();  // it was in this place
-        while (f.ok && in_use + nt > a.units) {
+        while (f.ok && in_use + g.tokens > a.units) {
           f.ok = wait_phase(&S.empty[done.s], done.parity, S, a.status);
           pop();
         }
         if (!f.ok) return;
         const int from = c * ch.cb * block, n = min(ch.cb * block, total - from);
-        uint64_t* bar = &S.full[f.cur.s];
-        ptx::mbar_arrive_expect_tx(bar, nt * n);
-        for (int q = 0; q < nt; ++q) {
+        uint64_t* bar = &f.S.full[f.cur.s];
+        ptx::mbar_arrive_expect_tx(bar, g.tokens * n);
+        for (int q = 0; q < g.tokens; ++q) {
           bulk_load(units + (size_t)at * a.unit, src + (size_t)q * a.ldh * 6 + from, n, bar);
           if (++at == a.units) at = 0;
         }
-        S.stage_units[f.cur.s] = (uint8_t)nt;
-        in_use += nt;
+        S.stage_units[f.cur.s] = (uint8_t)g.tokens;
+        in_use += g.tokens;
         ++flight;
         f.end();
       }
+      s += g.n;
     }
 }
 
-// One expert's chunks, W_down times h of its tokens, for N of them (the ranks `rank` on among the
-// expert's tokens) at a time. A token's three pieces are the MMA's columns 0-2 (and 4-6), column 3 is
-// zero. acc[tile][0], [1]: row 8 tile + g, the tokens t and t + 4 in lane 4 g + t.
-template <int FMT, int NI, int N>
-__device__ __forceinline__ void expert_blocks(const FewArgs& a, const FewChunks& ch, uint32_t st, uint32_t units,
-                                              int unit, uint32_t mask, int b0, int nb, int K, int nr, int wt,
-                                              int lane, float (&acc)[NI][2]) {
+// W_down times h of an expert's tokens, for the blocks wt, wt + step, ... of a stage. The three
+// pieces of h of a token are three columns of the MMA. A warp adds its sums to its own
+// S.out[warp][row][token]; `open` multiplies them (the shared expert's gate).
+//
+// bf16 weights: mma_rows, N tokens (the lowest of `mask`) at a time, their units from `unit` on.
+template <int NI, int N>
+__device__ __forceinline__ void down_bf16(const FewArgs& a, FewShared& S, uint32_t st, uint32_t units, int unit,
+                                          uint32_t mask, int nb, int nr, int wt, int step, bool gated, int warp,
+                                          int lane) {
   const int g = lane >> 2, t4 = lane & 3, piece = (g & 3) < 3;
+  const bool low = g < 4;
   // rows behind the pass read its last one: only the last tile can have any
   const uint32_t row = 64 * g + 16 * t4, last = 64 * min(8 * (NI - 1) + g, nr - 1) + 16 * t4;
   uint32_t wp = st + 64 * wt * a.rows, hu[N];
-  uint2 x[N];
+  uint4 x[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     int u = unit + n;
     if (u >= a.units) u -= a.units;
-    hu[n] = units + u * a.unit + 64 * (g & 3) + 16 * t4 + 8 * (g >> 2) + wt * (FMT >= 0 ? 768 : 192);
-    x[n] = make_uint2(0u, 0u);
+    hu[n] = units + u * a.unit + 64 * (g & 3) + 16 * t4 + wt * 192;
+    x[n] = make_uint4(0u, 0u, 0u, 0u);
   }
   float sum[N][NI][4] = {};
-  if constexpr (FMT >= 0) {
-    const uint32_t sp = st + round128(a.rows * 64 * ch.cb);
-    for (int b = wt; b < nb; b += kFewTeam, wp += 64 * kFewTeam * a.rows) {
-      uint4 w[NI];
-      uint2 sc[NI];
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        w[i] = lds_v4(wp + (i < NI - 1 ? row + 512 * i : last));
-        sc[i] = w4_block_scales<FMT>(sp + (i < NI - 1 ? 8 * i + g : min(8 * i + g, nr - 1)) * ch.sc, b);
-      }
-      const int parts = min(4, K / 32 - 4 * (b0 + b));
-      float d[N][NI][4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j >= 2 && j >= parts) break;  // K is a multiple of 64: two parts or four
-#pragma unroll
-        for (int n = 0; n < N; ++n) lds_v2_if(x[n], hu[n] + 192 * j, piece);
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const uint4 pw = w4_pairs<false>((&w[i].x)[j]);
-          const float f = w4_scale(sc[i], j);
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            // the parts of a group share a chain and a scale
-            if (j % (1 << FMT) == 0) mma_rows<true>(d[n][i], pw, x[n]);
-            else mma_rows<false>(d[n][i], pw, x[n]);
-            if ((j + 1) % (1 << FMT) == 0 || (j == 1 && parts == 2))
-#pragma unroll
-              for (int q = 0; q < 4; ++q) sum[n][i][q] = fmaf(d[n][i][q], f, sum[n][i][q]);
-          }
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < N; ++n) hu[n] += 768 * kFewTeam;
-    }
-  } else {
 #pragma unroll 5
-    for (int b = wt; b < nb; b += kFewTeam, wp += 64 * kFewTeam * a.rows) {
+  for (int b = wt; b < nb; b += step, wp += 64 * step * a.rows) {
+    uint2 y[N];
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        lds_v2_if(x[n], hu[n], piece);
-        hu[n] += 192 * kFewTeam;
-      }
+    for (int n = 0; n < N; ++n) {
+      lds_v4_if(x[n], hu[n], piece);
+      y[n] = make_uint2(low ? x[n].x : x[n].y, low ? x[n].z : x[n].w);
+      hu[n] += 192 * step;
+    }
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const uint4 w = lds_v4(wp + (i < NI - 1 ? row + 512 * i : last));
+    for (int i = 0; i < NI; ++i) {
+      const uint4 w = lds_v4(wp + (i < NI - 1 ? row + 512 * i : last));
 #pragma unroll
-        for (int n = 0; n < N; ++n) mma_rows<false>(sum[n][i], w, x[n]);
-      }
+      for (int n = 0; n < N; ++n) mma_rows<false>(sum[n][i], w, y[n]);
     }
   }
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     const int token = __ffs(mask) - 1;
     mask &= mask - 1;
+    const float open = gated ? S.sgate[token] : 1.f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       float v0, v1;
       fold(sum[n][i], t4 < 2, v0, v1);
       float v = v0 + (t4 & 1 ? 0.f : v1);  // third piece, or first and second
       v += __shfl_xor_sync(0xffffffffu, v, 1);
-      if ((token & 3) == t4) {
-        if (token < 4) acc[i][0] += v;
-        else acc[i][1] += v;
+      if (t4 == 0) S.out[warp][8 * i + g][token] += open * v;
+    }
+  }
+}
+
+// 4-bit weights: the MMA's A is 16 rows, its columns 0-2 and 4-6 are one or two tokens' pieces.
+template <int FMT, int NP>
+__device__ __forceinline__ void down_w4(const FewArgs& a, FewShared& S, const FewChunks& ch, uint32_t st,
+                                        uint32_t units, int unit, uint32_t mask, int c, int nb, int nr, int wt,
+                                        int step, int warp, int lane) {
+  const int g = lane >> 2, t4 = lane & 3, K = a.I, b0 = c * ch.cb;
+  const bool two = mask & (mask - 1);
+  const int piece = (g & 3) < 3 && (g < 4 || two);
+  int u = unit + (g >> 2);
+  if (u >= a.units) u -= a.units;
+  uint32_t hu = units + u * a.unit + 64 * (g & 3) + 16 * t4 + wt * 768;
+  uint32_t wp = st + 64 * wt * a.rows + 16 * t4;
+  const uint32_t sp = st + round128(a.rows * 64 * ch.cb) + (ch.scale_at(c, FMT) & 15);
+  uint32_t row[2 * NP];  // rows behind the pass read its last one
+#pragma unroll
+  for (int i = 0; i < 2 * NP; ++i) row[i] = min(8 * i + g, nr - 1);
+  uint4 x = make_uint4(0u, 0u, 0u, 0u);
+  float sum[NP][4] = {};
+  for (int b = wt; b < nb; b += step, wp += 64 * step * a.rows, hu += 768 * step) {
+    uint4 w[2 * NP];
+    uint2 sc[2 * NP];
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i) {
+      w[i] = lds_v4(wp + 64 * row[i]);
+      sc[i] = w4_block_scales<FMT>(sp + row[i] * ch.sc, b);
+    }
+    const int parts = min(4, K / 32 - 4 * (b0 + b));
+    float d[NP][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j >= 2 && j >= parts) break;  // K is a multiple of 64: two parts or four
+      lds_v4_if(x, hu + 192 * j, piece);
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const uint4 v = w4_pairs<false>(word(w[2 * p], j)), v8 = w4_pairs<false>(word(w[2 * p + 1], j));
+        // the parts of a group share a chain and a scale
+        if (j % (1 << FMT) == 0) mma16816_first<false>(d[p], v.x, v8.x, v.y, v8.y, x.x, x.y);
+        else mma16816<false>(d[p], v.x, v8.x, v.y, v8.y, x.x, x.y);
+        mma16816<false>(d[p], v.z, v8.z, v.w, v8.w, x.z, x.w);
+        if ((j + 1) % (1 << FMT) == 0 || (j == 1 && parts == 2)) {
+          const float f = w4_scale(sc[2 * p], j), f8 = w4_scale(sc[2 * p + 1], j);
+          sum[p][0] = fmaf(d[p][0], f, sum[p][0]);
+          sum[p][1] = fmaf(d[p][1], f, sum[p][1]);
+          sum[p][2] = fmaf(d[p][2], f8, sum[p][2]);
+          sum[p][3] = fmaf(d[p][3], f8, sum[p][3]);
+        }
       }
     }
   }
+  // lanes t = 0, 1: the first token's pieces 0 and 1, and 2; t = 2, 3: the second's
+  const int token = t4 < 2 ? __ffs(mask) - 1 : __ffs(mask & (mask - 1)) - 1;
+#pragma unroll
+  for (int i = 0; i < 2 * NP; ++i) {
+    float v = sum[i / 2][2 * (i % 2)] + (t4 & 1 ? 0.f : sum[i / 2][2 * (i % 2) + 1]);
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    if (t4 == 0 || (t4 == 2 && two)) S.out[warp][8 * i + g][token] += v;
+  }
 }
 
+// One expert's share of a stage: warps wt, wt + 1, ... of `step` take its blocks in turn.
 template <int FMT, int NI>
-__device__ __forceinline__ void expert_sums(const FewArgs& a, FewShared& S, const FewChunks& ch, uint32_t ring,
-                                            Place& at, int first, uint32_t units, int unit, int K, uint32_t mask,
-                                            int nr, int warp, int lane, float (&acc)[NI][2]) {
-  const int wt = warp & (kFewTeam - 1), nt = __popc(mask);
-  for (; at.i < first + ch.n; at.next(a.stages)) {
-    const uint32_t st = ring + at.cur.s * a.stage_bytes;
-    const int c = at.i - first, b0 = c * ch.cb, nb = min(ch.cb, ch.blocks - b0);
-    int u = unit + c * nt;
-    while (u >= a.units) u -= a.units;
-    wait_phase(&S.full[at.cur.s], at.cur.parity, S, a.status);
-    uint32_t left = mask;
-    while (left & (left - 1)) {  // two tokens at a time
-      expert_blocks<FMT, NI, 2>(a, ch, st, units, u, left, b0, nb, K, nr, wt, lane, acc);
-      left &= left - 1;
-      left &= left - 1;
-      u += 2;
-      if (u >= a.units) u -= a.units;
-    }
-    if (left) expert_blocks<FMT, NI, 1>(a, ch, st, units, u, left, b0, nb, K, nr, wt, lane, acc);
+__device__ __forceinline__ void down_stage(const FewArgs& a, FewShared& S, const FewChunks& ch, uint32_t st,
+                                           uint32_t units, int unit, uint32_t mask, int c, bool gated, int nr,
+                                           int wt, int step, int warp, int lane) {
+  const int nb = min(ch.cb, ch.blocks - c * ch.cb);
+  for (uint32_t left = mask; left;) {  // two tokens at a time
+    if constexpr (FMT >= 0)
+      down_w4<FMT, (NI + 1) / 2>(a, S, ch, st, units, unit, left, c, nb, nr, wt, step, warp, lane);
+    else if (left & (left - 1))
+      down_bf16<NI, 2>(a, S, st, units, unit, left, nb, nr, wt, step, gated, warp, lane);
+    else
+      down_bf16<NI, 1>(a, S, st, units, unit, left, nb, nr, wt, step, gated, warp, lane);
+    left &= left - 1;
+    left &= left - 1;
+    unit += 2;
+    if (unit >= a.units) unit -= a.units;
+  }
+}
+
+// One pass of NI row tiles. The teams take the stages in turn; a stage of one expert is shared by the
+// team, of a stage of several each warp takes one.
+template <int FMT, int NI>
+__device__ __forceinline__ void down_pass(const FewArgs& a, FewShared& S, uint32_t ring, Place& at, int& turn,
+                                          uint32_t units, int& unit, int nr, int warp, int lane) {
+  const int team = warp / kFewTeam, wt = warp & (kFewTeam - 1);
+  for (int i = lane; i < kFewRows * kFewMaxT; i += 32) (&S.out[warp][0][0])[i] = 0.f;
+  __syncwarp();
+  auto skip = [&](int tokens) {
+    turn = turn + 1 == kFewTeams ? 0 : turn + 1;
+    unit += tokens;
+    if (unit >= a.units) unit -= a.units;
+    at.skip(1, a.stages);
+  };
+  auto release = [&] {
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&S.empty[at.cur.s]);
+  };
+  for (int c = 0; c < a.dn_s.n; ++c) {
+    if (turn == team) {
+      wait_stage(at, S, a.status);
+      down_stage<-1, NI>(a, S, a.dn_s, ring + at.cur.s * a.stage_bytes, units, unit, (1u << a.T) - 1u, c, true, nr,
+                         wt, kFewTeam, warp, lane);
+      release();
+    }
+    skip(a.T);
   }
-}
-
-// One pass of NI row tiles.
-template <int FMT, int NI>
-__device__ __forceinline__ void down_pass(const FewArgs& a, FewShared& S, uint32_t ring, Place& at, int& stage,
-                                          uint32_t units, int& unit, int nr, int warp, int lane) {
-  const int g = lane >> 2, t4 = lane & 3;
-  float acc[NI][2] = {};
-  expert_sums<-1, NI>(a, S, a.dn_s, ring, at, stage, units, unit, a.Is, (1u << a.T) - 1u, nr, warp, lane, acc);
-  stage += a.dn_s.n;
-  for (unit += a.dn_s.n * a.T; unit >= a.units;) unit -= a.units;
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {  // the shared expert's gate
-    acc[i][0] *= S.sgate[t4];
-    acc[i][1] *= S.sgate[4 + t4];
-  }
-  for (int s = 1; s < S.n_act; ++s) {
-    const uint32_t m = S.act_mask[s];
-    if (at.i < stage + a.dn.n)  // this team has a stage of the expert
-      expert_sums<FMT, NI>(a, S, a.dn, ring, at, stage, units, unit, a.I, m, nr, warp, lane, acc);
-    stage += a.dn.n;
-    for (unit += a.dn.n * __popc(m); unit >= a.units;) unit -= a.units;
-  }
-  float* red = &S.red[0][0][0];  // [warp][row][token]
-  sync_consumers();
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    float* to = red + (warp * kFewRows + 8 * i + g) * kFewMaxT + t4;
-    to[0] = acc[i][0];
-    to[4] = acc[i][1];
+  for (int s = 1; s < S.n_act;) {
+    const Group g = group_at(a, S, s);
+    for (int c = 0; c < a.dn.n; ++c) {
+      if (turn == team) {
+        const uint32_t st = ring + at.cur.s * a.stage_bytes;
+        wait_stage(at, S, a.status);
+        if (g.n == 1) {
+          down_stage<FMT, NI>(a, S, a.dn, st, units, unit, S.act_mask[s], c, false, nr, wt, kFewTeam, warp, lane);
+        } else if (wt < g.n) {
+          int u = unit;
+          for (int j = 0; j < wt; ++j) u += __popc(S.act_mask[s + j]);
+          if (u >= a.units) u -= a.units;
+          down_stage<FMT, NI>(a, S, a.dn, st + wt * a.slot, units, u, S.act_mask[s + wt], c, false, nr, 0, 1, warp,
+                              lane);
+        }
+        release();
+      }
+      skip(g.tokens);
+    }
+    s += g.n;
   }
 }
 
 template <int FMT>
-__device__ void down_rows(const FewArgs& a, FewShared& S, uint32_t ring, Place& at, int stage, uint32_t units) {
+__device__ void down_rows(const FewArgs& a, FewShared& S, uint32_t ring, Place& at, int& turn, uint32_t units) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const float* red = &S.red[0][0][0];
   const int n1 = row_begin(a, blockIdx.x + 1);
   int unit = 0;
   for (int r0 = row_begin(a, blockIdx.x); r0 < n1; r0 += a.rows) {
     const int nr = min(a.rows, n1 - r0);
-    if (nr > 24) down_pass<FMT, 4>(a, S, ring, at, stage, units, unit, nr, warp, lane);
-    else if (nr > 16) down_pass<FMT, 3>(a, S, ring, at, stage, units, unit, nr, warp, lane);
-    else if (nr > 8) down_pass<FMT, 2>(a, S, ring, at, stage, units, unit, nr, warp, lane);
-    else down_pass<FMT, 1>(a, S, ring, at, stage, units, unit, nr, warp, lane);
+    if (nr > 24) down_pass<FMT, 4>(a, S, ring, at, turn, units, unit, nr, warp, lane);
+    else if (nr > 16) down_pass<FMT, 3>(a, S, ring, at, turn, units, unit, nr, warp, lane);
+    else if (nr > 8) down_pass<FMT, 2>(a, S, ring, at, turn, units, unit, nr, warp, lane);
+    else down_pass<FMT, 1>(a, S, ring, at, turn, units, unit, nr, warp, lane);
     sync_consumers();
     const int r = tid % kFewRows, t = tid / kFewRows;
     if (t < a.T && r < nr) {
       float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) sum += red[(w * kFewRows + r) * kFewMaxT + t];
+      for (int w = 0; w < kFewWarps; ++w) sum += S.out[w][r][t];
       a.out[(size_t)t * a.H + r0 + r] = sum;
     }
+    if (r0 + a.rows < n1) sync_consumers();  // S.out is read
   }
 }
 
@@ -895,6 +1008,7 @@ __device__ void feed_router(Feeder& f, uint8_t* xs, int xpitch, bool h) {
         const int k = c * r.chunk, n = min(r.chunk, a.H - k);
         const bool gate = e == a.E;
         const void* src = gate ? static_cast<const void*>(a.wsg + k) : a.w_router + (size_t)e * a.H + k;
+        f.tag();
         ptx::mbar_arrive_expect_tx(bar, n * (gate ? 2 : 4));
         bulk_load(dst, src, n * (gate ? 2 : 4), bar);
       }
@@ -922,8 +1036,8 @@ __device__ __forceinline__ double warp_sums(double (&v)[N], int lane) {
 // Logits, in 64 bits: a team takes a stage, a thread four elements at a time. TT: tokens, rounded
 // up to a power of two.
 template <int TT>
-__device__ __forceinline__ void router_logits(const FewArgs& a, FewShared& S, uint8_t* xs, int xpitch,
-                                              const uint8_t* ring, Place& at, int& stage) {
+__device__ __forceinline__ void router_logits(const FewArgs& a, FewShared& S, const uint8_t* xs, int xpitch,
+                                              const uint8_t* ring, Place& at) {
   constexpr int log_t = TT == 1 ? 0 : TT == 2 ? 1 : TT == 4 ? 2 : 3;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, in_team = tid & (32 * kFewTeam - 1);
   const RouterRows r = router_rows(a);
@@ -932,12 +1046,13 @@ __device__ __forceinline__ void router_logits(const FewArgs& a, FewShared& S, ui
   const bool mine = my_e < r.e1;
   const float bias = mine && my_e < a.E && a.bias ? __ldg(a.bias + my_e) : 0.f;
   wait_phase(&S.x_full, 0u, S, a.status);
-  for (; at.i < end; at.next(a.stages)) {
-    const uint8_t* st = ring + (size_t)at.cur.s * a.stage_bytes;
-    const int c = at.i % r.n, k0 = c * r.chunk, n = min(r.chunk, a.H - k0);
-    const bool gate = r.e0 + at.i / r.n == a.E;
+  Place mine_at = at;
+  for (mine_at.skip(warp / kFewTeam, a.stages); mine_at.i < end; mine_at.skip(kFewTeams, a.stages)) {
+    const uint8_t* st = ring + (size_t)mine_at.cur.s * a.stage_bytes;
+    const int c = mine_at.i % r.n, k0 = c * r.chunk, n = min(r.chunk, a.H - k0);
+    const bool gate = r.e0 + mine_at.i / r.n == a.E;
     double acc[TT] = {};
-    wait_phase(&S.full[at.cur.s], at.cur.parity, S, a.status);
+    wait_stage(mine_at, S, a.status);
     for (int k = 4 * in_team; k < n; k += 128 * kFewTeam) {
       float w[4];
       if (gate) {
@@ -960,20 +1075,12 @@ __device__ __forceinline__ void router_logits(const FewArgs& a, FewShared& S, ui
     const double v = warp_sums<TT>(acc, lane);
     const int t = lane >> (5 - log_t);
     if ((lane & ((32 >> log_t) - 1)) == 0 && t < a.T)
-      S.part[(at.i * kFewTeam + (warp & (kFewTeam - 1))) * a.T + t] = v;
+      S.part[(mine_at.i * kFewTeam + (warp & (kFewTeam - 1))) * a.T + t] = v;
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&S.empty[at.cur.s]);
+    if (lane == 0) ptx::mbar_arrive(&S.empty[mine_at.cur.s]);
   }
-  stage = end;
+  at.skip(end, a.stages);
   sync_consumers();
-  // x for mma_rows from here on: the words of 16 bytes in the order 0, 2, 1, 3
-  for (int i = tid; i < a.T * (a.H / 8); i += kFewThreads) {
-    const int t = i / (a.H / 8);
-    uint2* p = reinterpret_cast<uint2*>(xs + (size_t)t * xpitch + 16 * (i - t * (a.H / 8)));
-    const uint2 lo = p[0], hi = p[1];
-    p[0] = make_uint2(lo.x, hi.x);
-    p[1] = make_uint2(lo.y, hi.y);
-  }
   if (mine) {
     double l = 0.0;
     for (int c = 0; c < r.n; ++c)
@@ -1013,14 +1120,13 @@ __device__ void route(const FewArgs& a, FewShared& S, uint8_t* ring, int warp, i
 template <int FMT>
 __device__ void consume(const FewArgs& a, FewShared& S, uint8_t* xs, int xpitch, uint8_t* ring) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  Place at{warp / kFewTeam, {0, 0u}};
-  for (at.cur.s = at.i; at.cur.s >= a.stages; at.cur.s -= a.stages) at.cur.parity ^= 1u;
-  int stage = 0;
+  Place at{0, {0, 0u}};
+  int turn = 0;  // the team that takes the next tile; down: the first warp of the next stage's group
   for (int e = tid; e < a.E; e += kFewThreads) S.mask[e] = 0;
   if (tid < kFewMaxT) S.sgate[tid] = 0.f;
-  if (a.T == 1) router_logits<1>(a, S, xs, xpitch, ring, at, stage);
-  else if (a.T <= 4) router_logits<4>(a, S, xs, xpitch, ring, at, stage);
-  else router_logits<8>(a, S, xs, xpitch, ring, at, stage);
+  if (a.T == 1) router_logits<1>(a, S, xs, xpitch, ring, at);
+  else if (a.T <= 4) router_logits<4>(a, S, xs, xpitch, ring, at);
+  else router_logits<8>(a, S, xs, xpitch, ring, at);
   grid_arrive(a.sync);
 
   const uint32_t xs_at = ptx::smem_u32(xs), ring_at = ptx::smem_u32(ring);
@@ -1032,13 +1138,15 @@ __device__ void consume(const FewArgs& a, FewShared& S, uint8_t* xs, int xpitch,
       route(a, S, ring, warp, lane);
       end += (S.n_act - 1) * (a.I / 8);
     }
-    if (a.T <= 4) gate_up_tiles<FMT, 1>(a, S, xs_at, xpitch, ring_at, at, stage, tile, end);
-    else gate_up_tiles<FMT, 2>(a, S, xs_at, xpitch, ring_at, at, stage, tile, end);
+    if (a.T <= 4) gate_up_tiles<FMT, 1>(a, S, xs_at, xpitch, ring_at, at, tile, turn, end);
+    else gate_up_tiles<FMT, 2>(a, S, xs_at, xpitch, ring_at, at, tile, turn, end);
   }
 
-  // h of this CTA is written; that of the others comes through the ring
+  // h of this CTA is written (for bulk copies to read); that of the others comes through the ring
+  asm volatile("fence.proxy.async.global;" ::: "memory");
   grid_arrive(a.sync + 1);
-  down_rows<FMT>(a, S, ring_at, at, stage, xs_at);
+  turn = 0;
+  down_rows<FMT>(a, S, ring_at, at, turn, xs_at);
 
   // the last CTA to leave makes the counters ready for the next call
   if (tid == 0) {
@@ -1088,6 +1196,7 @@ few_layer_kernel(const __grid_constant__ FewArgs a, const __grid_constant__ FewM
     }
     ptx::mbar_init(&S.x_full, 1);
     ptx::mbar_init(&S.logits_full, 1);
+    for (int i = 0; i < a.stages; ++i) S.tag[i] = -1;
     S.aborted = 0;
     ptx::fence_mbar_init();
   }
@@ -1109,16 +1218,16 @@ FewChunks few_chunks(int K, int rows, bool w4, int shift, int stage, int limit) 
   FewChunks c;
   c.blocks = w4 ? (int)w4_blocks(K) : K / 32;
   const int per = rows * (64 + (w4 ? 8 >> shift : 0));
-  const int most = std::min((stage - 128 - (w4 ? 16 * rows : 0)) / per, limit);
+  const int most = std::min((stage - 128 - (w4 ? 32 * rows : 0)) / per, limit);
   c.n = (c.blocks + most - 1) / most;
   c.cb = (c.blocks + c.n - 1) / c.n;
-  if (w4 && c.n > 1) {  // a chunk's scales start on 16 bytes
-    const int unit = 2 << shift;
-    c.cb = (c.cb + unit - 1) / unit * unit;
-    if (c.cb > most) c.cb = most / unit * unit;
-  }
   c.n = (c.blocks + c.cb - 1) / c.cb;
-  c.sc = w4 ? ((c.cb * 8 >> shift) + 15) / 16 * 16 : 0;
+  if (w4) {  // a box starts on 16 bytes of a row's scales: chunks that do not bring some more
+    const int bytes = c.cb * 8 >> shift;
+    c.sc = (bytes + 15) / 16 * 16 + (c.n > 1 && bytes % 16 ? 16 : 0);
+  } else {
+    c.sc = 0;
+  }
   return c;
 }
 
@@ -1178,19 +1287,15 @@ cudaError_t launch_few_layer(const moe_shape& s, const Layout& L, char* ws, cons
   a.status = reinterpret_cast<uint32_t*>(ws + L.status);
   a.T = s.T; a.H = s.H; a.E = s.E; a.k = s.k; a.I = s.I; a.Is = s.Is;
 
-  // rows of a pass: what the accumulators hold, and with scales for 128 weights what leaves room
-  // for eight blocks (16 bytes of their scales) in the smaller stage
-  const int cap = a.shift == 2 ? 28 : kFewRows;
+  const int cap = kFewRows;
   const int most_rows = (s.H + sms - 1) / sms, passes = (most_rows + cap - 1) / cap;
   a.rows = (most_rows + passes - 1) / passes;
-  // Eight stages, four where x leaves less room: a multiple of the teams, so that a slot of the
-  // ring always belongs to the same team. (A team that came to another's slot could find the
-  // barrier one phase behind, which looks like the phase it waits for.)
   const int x_bytes = s.T * (2 * s.H + 64);
-  for (a.stages = 6;; a.stages -= kFewTeams) {
-    // the units of h take their size from the chunks, and the stages what they leave: settled in
-    // a few rounds from above
-    for (a.stage_bytes = 24576;; a.stage_bytes -= 1024) {
+  // bf16: six stages of 24 KB, which keep a 20-block chunk of a gate|up tile or of a block's output rows;
+  // 4-bit: twice as many of half the size. Smaller and then fewer where x leaves less room.
+  const int most_bytes = 24576, least_bytes = q ? 7168 : 15360;
+  for (a.stages = 6;; --a.stages) {
+    for (a.stage_bytes = most_bytes;; a.stage_bytes -= 1024) {
       a.gu_s = few_chunks(s.H, 16, false, 0, a.stage_bytes, 32);
       a.gu = few_chunks(s.H, 16, q != nullptr, a.shift, a.stage_bytes, 32);
       // the limit keeps a unit of h near 6 KB
@@ -1200,12 +1305,16 @@ cudaError_t launch_few_layer(const moe_shape& s, const Layout& L, char* ws, cons
       a.unit = std::max(a.dn_s.cb * 192, a.dn.cb * (q ? 768 : 192)) | 64;
       a.h_bytes = (std::max(x_bytes, (s.T + 4) * a.unit) + 127) / 128 * 128;
       if (kFewSharedBytes + a.h_bytes + (size_t)a.stages * a.stage_bytes <= kFewSmem) break;
-      if (a.stage_bytes <= kFewMinStage) break;
+      if (a.stage_bytes <= least_bytes) break;
     }
-    a.units = std::min(a.h_bytes / a.unit, 64);
     if (kFewSharedBytes + a.h_bytes + (size_t)a.stages * a.stage_bytes <= kFewSmem) break;
-    if (a.stages <= 4) return cudaErrorInvalidValue;
+    if (a.stages <= 3) return cudaErrorInvalidValue;
   }
+  // what is left holds more units of h: several groups of experts in flight
+  a.h_bytes = ((int)kFewSmem - (int)kFewSharedBytes - a.stages * a.stage_bytes) / 128 * 128;
+  a.units = std::min(a.h_bytes / a.unit, 64);
+  a.slot = (a.rows * 64 * a.dn.cb + 127) / 128 * 128 + (a.rows * a.dn.sc + 127) / 128 * 128;
+  a.group = a.dn.n == 1 ? std::min(a.stage_bytes / a.slot, kFewTeam) : 1;
 
   FewMaps m;
   bool ok = few_weight_map(&m.gu_s, w.ws_gate_up, s.Is, a.gu_s, 2 * (uint64_t)s.H, 2, 1, 8) &&

@@ -69,9 +69,6 @@ __device__ __forceinline__ void mma_rows(float (&d)[4], const uint4& w, const ui
   if constexpr (FIRST) mma16816_first<false>(d, w.x, w.y, w.z, w.w, x.x, x.y);
   else mma16816<false>(d, w.x, w.y, w.z, w.w, x.x, x.y);
 }
-// Where the four words of a column's 16 bytes are kept for it: 0, 2, 1, 3.
-__host__ __device__ __forceinline__ int mma_rows_word(int i) { return (i & 1) * 2 + (i >> 1); }
-
 // 8 weight rows by 32 elements as B, 16 rows of x as A: two quads {x[g], x[g + 8]} x {registers 0, 1}
 // and x {registers 2, 3}. D: d[0], d[1]: row g of x, weight rows 2 t and 2 t + 1; d[2], d[3]: row g + 8.
 template <bool F16>
@@ -80,7 +77,9 @@ __device__ __forceinline__ void mma_cols(float (&d)[4], const uint4& x0, const u
   mma16816<F16>(d, x1.x, x1.y, x1.z, x1.w, w.z, w.w);
 }
 
-// Shared memory by 32-bit address; lds_v2_if leaves v as it is where p is 0.
+__device__ __forceinline__ uint32_t word(const uint4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
+
+// Shared memory by 32-bit address; the _if forms leave v as it is where p is 0.
 __device__ __forceinline__ uint4 lds_v4(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
@@ -90,6 +89,11 @@ __device__ __forceinline__ uint2 lds_v2(uint32_t at) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
   return v;
+}
+__device__ __forceinline__ void lds_v4_if(uint4& v, uint32_t at, int p) {
+  asm volatile("{\n .reg .pred q;\n setp.ne.s32 q, %5, 0;\n @q ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n}\n"
+               : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+               : "r"(at), "r"(p));
 }
 __device__ __forceinline__ void lds_v2_if(uint2& v, uint32_t at, int p) {
   asm volatile("{\n .reg .pred q;\n setp.ne.s32 q, %3, 0;\n @q ld.shared.v2.u32 {%0,%1}, [%2];\n}\n"
