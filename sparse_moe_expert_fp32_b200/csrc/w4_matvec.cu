@@ -2,15 +2,17 @@
 //
 //   y[t, n] = sum_k x[t, k] (c[n, k] - 8) s[n, k / group]
 //
-// Bound by the weight bytes, 1/2 + 2/group each. CTA b of the grid owns the matrix rows
-// [b N / grid, (b + 1) N / grid) and takes them 32 at a time (four tiles of 8); its 16 warps
-// split the row's 128-element blocks, so a CTA has no partner to wait for and small matrices
-// still spread over all SMs. x is staged in shared memory once per K chunk. The codes enter
-// the MMA as exact integers, a 32-element part at a time; its fp32 sum is multiplied by the
-// part's scale and added to the running fp32 sums, so no product or weight is rounded.
+// Bound by the weight bytes, 1/2 + 2/group each, and close to it by the arithmetic that makes
+// MMA operands of them. A group of warps takes 32 matrix rows (16 if there are few) and splits
+// their 128-element blocks; the fewer rows there are, the more warps a group has, so that small
+// matrices still spread over all SMs without a second launch. The codes are loaded straight to
+// registers, two blocks (128 bytes a row) ahead; x is staged in shared memory. The MMA's A is 16
+// matrix rows, made in registers, its columns are 8 rows of x. The codes enter as exact
+// integers; the fp32 sum over a scale group is multiplied by the scale and added to the running
+// fp32 sums, so no product or weight is rounded.
 #include <cuda_fp16.h>
 
-#include <mutex>
+#include <algorithm>
 
 #include "moe_internal.h"
 #include "w4.cuh"
@@ -20,9 +22,7 @@ namespace {
 
 constexpr int kMvWarps = 16;
 constexpr int kMvThreads = kMvWarps * 32;
-constexpr int kMvRows = 32;
-constexpr int kMvChunkRows = 512;  // most rows of a CTA when K is taken in chunks
-constexpr int kMvXBytes = 131072;  // staged x, without the pitch's padding
+constexpr int kMvXBytes = 163840;  // staged x; what is longer comes in K chunks
 
 struct MvArgs {
   const uint16_t* x;
@@ -31,93 +31,174 @@ struct MvArgs {
   const uint16_t* s;
   void* y;
   int64_t ldy;
-  int64_t N, K;
+  int64_t N, K, groups;
   int64_t row_bytes, row_scales;
-  int T, shift, kc, y_f32;
+  int T, kc, split, y_f32;  // split: warps of a row group
 };
 
-template <bool F16, int NT>
-__global__ void __launch_bounds__(kMvThreads)
-matvec_w4_kernel(const MvArgs a) {
-  extern __shared__ uint4 smem[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-  const int64_t n0 = blockIdx.x * a.N / gridDim.x, n1 = (blockIdx.x + 1) * a.N / gridDim.x;
-  const int pitch = 2 * a.kc + 64;  // 64 mod 128: two tokens' 64-byte reads share no bank
-  uint8_t* xs = reinterpret_cast<uint8_t*>(smem);
-  float* red = reinterpret_cast<float*>(xs + (size_t)a.T * pitch);  // [warp][row][NT * 8]
-  float* sums = red + kMvWarps * kMvRows * NT * 8;                  // [rows of the CTA][NT * 8], if K is chunked
-  const bool chunked = a.K > a.kc;
+// Two blocks of 16 NP rows: row[i] is this lane's row 8 i + g.
+template <int NP>
+struct MvTile {
+  uint4 w[2][2 * NP];
+  uint2 s[2][2 * NP];
+};
 
-  for (int64_t k0 = 0; k0 < a.K; k0 += a.kc) {
-    const int kn = (int)min((int64_t)a.kc, a.K - k0);
-    const int nb = (int)w4_blocks(kn);
-    if (k0) __syncthreads();  // every warp is done with the last chunk of x
-    for (int i = tid; i < a.T * nb * kW4Block; i += kMvThreads) {
-      const int t = i / (nb * kW4Block), k = i - t * (nb * kW4Block);
-      const uint16_t v = k < kn ? __ldg(a.x + t * a.ldx + k0 + k) : (uint16_t)0;
-      *reinterpret_cast<uint16_t*>(xs + (size_t)t * pitch + 2 * k) = v;
+template <bool F16, int SHIFT, int NP>
+__device__ __forceinline__ void mv_load(MvTile<NP>& m, const MvArgs& a, const uint8_t* const (&q)[2 * NP],
+                                        const uint16_t* const (&s)[2 * NP], int64_t b, int64_t last) {
+#pragma unroll
+  for (int i = 0; i < 2 * NP; ++i)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t bu = min(b + u, last);
+      m.w[u][i] = ld_stream_v4(q[i] + bu * kW4BlockBytes);
+      m.s[u][i] = w4_block_scales(s[i], (int)bu, SHIFT);
     }
-    __syncthreads();
-    for (int64_t r0 = n0; r0 < n1; r0 += kMvRows) {
-      const int nr = (int)min((int64_t)kMvRows, n1 - r0);
-      float acc[4][4] = {};
-      for (int b = warp; b < nb; b += kMvWarps) {
-        const int64_t kb = k0 / kW4Block + b;
-        uint4 q[4];
+}
+
+template <bool F16, int SHIFT, int NT, int NP>
+__device__ __forceinline__ void mv_block(const uint4 (&w)[2 * NP], const uint2 (&s)[2 * NP], uint32_t xp, int pitch,
+                                         const int (&tok)[NT], float (&acc)[NP][NT][4]) {
+  float d[NP][NT][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          q[i] = ld_stream_v4(a.q + (r0 + min(g + 8 * i, nr - 1)) * a.row_bytes + kb * kW4BlockBytes + 16 * t4);
+  for (int j = 0; j < 4; ++j) {
+    uint4 x[NT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (8 * i >= nr) break;
-          const uint2 s0 = w4_block_scales(a.s + (r0 + min(8 * i + 2 * t4, nr - 1)) * a.row_scales, (int)kb, a.shift);
-          const uint2 s1 = w4_block_scales(a.s + (r0 + min(8 * i + 2 * t4 + 1, nr - 1)) * a.row_scales, (int)kb, a.shift);
+    for (int n = 0; n < NT; ++n) {
+      x[n] = make_uint4(0u, 0u, 0u, 0u);
+      lds_v4_if(x[n], xp + 8 * n * pitch + 64 * j, tok[n]);
+    }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint8_t* xp = xs + (size_t)g * pitch + b * 256 + 64 * j + 16 * t4;
-            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-            const uint4 x0 = g < a.T ? *reinterpret_cast<const uint4*>(xp) : zero;
-            const uint4 x1 = g + 8 < a.T ? *reinterpret_cast<const uint4*>(xp + 8 * (size_t)pitch) : zero;
-            float d[4];
-            mma_cols<F16>(d, make_uint4(x0.x, x1.x, x0.y, x1.y), make_uint4(x0.z, x1.z, x0.w, x1.w),
-                          w4_pairs<F16>((&q[i].x)[j]));
-            acc[i][0] = fmaf(d[0], w4_scale(s0, j), acc[i][0]);
-            acc[i][1] = fmaf(d[1], w4_scale(s1, j), acc[i][1]);
-            acc[i][2] = fmaf(d[2], w4_scale(s0, j), acc[i][2]);
-            acc[i][3] = fmaf(d[3], w4_scale(s1, j), acc[i][3]);
-          }
+    for (int p = 0; p < NP; ++p) {
+      const uint4 v = w4_pairs<F16>(word(w[2 * p], j)), v8 = w4_pairs<F16>(word(w[2 * p + 1], j));
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        // the parts of a group share a chain and a scale
+        if (j % (1 << SHIFT) == 0) mma16816_first<F16>(d[p][n], v.x, v8.x, v.y, v8.y, x[n].x, x[n].y);
+        else mma16816<F16>(d[p][n], v.x, v8.x, v.y, v8.y, x[n].x, x[n].y);
+        mma16816<F16>(d[p][n], v.z, v8.z, v.w, v8.w, x[n].z, x[n].w);
+        if ((j + 1) % (1 << SHIFT) == 0) {
+          const float f = w4_scale(s[2 * p], j), f8 = w4_scale(s[2 * p + 1], j);
+          acc[p][n][0] = fmaf(d[p][n][0], f, acc[p][n][0]);
+          acc[p][n][1] = fmaf(d[p][n][1], f, acc[p][n][1]);
+          acc[p][n][2] = fmaf(d[p][n][2], f8, acc[p][n][2]);
+          acc[p][n][3] = fmaf(d[p][n][3], f8, acc[p][n][3]);
         }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (h == 0 || NT == 2) {
-            float* at = red + ((size_t)warp * kMvRows + 8 * i + 2 * t4) * (NT * 8) + 8 * h + g;
-            at[0] = acc[i][2 * h];
-            at[NT * 8] = acc[i][2 * h + 1];
-          }
-      __syncthreads();
-      for (int o = tid; o < kMvRows * NT * 8; o += kMvThreads) {
-        const int r = o % kMvRows, t = o / kMvRows;
-        if (r >= nr || t >= a.T) continue;
-        float v = 0.f;
-        for (int wi = 0; wi < kMvWarps; ++wi) v += red[((size_t)wi * kMvRows + r) * (NT * 8) + t];
-        if (chunked) {
-          float* at = sums + (size_t)(r0 - n0 + r) * (NT * 8) + t;
-          if (k0) v += *at;
-          *at = v;
-        }
-        if (k0 + a.kc >= a.K) {
-          const int64_t at = t * a.ldy + r0 + r;
-          if (a.y_f32) static_cast<float*>(a.y)[at] = v;
-          else if constexpr (F16) static_cast<__half*>(a.y)[at] = __float2half_rn(v);
-          else static_cast<uint16_t*>(a.y)[at] = f32_to_bf16_rn(v);
-        }
-      }
-      __syncthreads();
     }
   }
+}
+
+template <bool F16>
+__device__ __forceinline__ void mv_store(const MvArgs& a, int t, int64_t n, float v) {
+  const int64_t at = t * a.ldy + n;
+  if (a.y_f32) static_cast<float*>(a.y)[at] = v;
+  else if constexpr (F16) static_cast<__half*>(a.y)[at] = __float2half_rn(v);
+  else static_cast<uint16_t*>(a.y)[at] = f32_to_bf16_rn(v);
+}
+
+template <bool F16, int SHIFT, int NT, int NP>
+__global__ void __launch_bounds__(kMvThreads)
+matvec_w4_kernel(const MvArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+  const int pitch = 2 * a.kc + 64;  // 64 mod 128: two tokens' 64-byte reads share no bank
+  float* red = reinterpret_cast<float*>(smem + (size_t)a.T * pitch);  // [warp][row][NT * 8]
+  const uint32_t xs = (uint32_t)__cvta_generic_to_shared(smem) + g * pitch + 16 * t4;
+  const int part = warp % a.split, per_cta = kMvWarps / a.split;
+  int tok[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) tok[n] = 8 * n + g < a.T;
+
+  for (int64_t first = (int64_t)blockIdx.x * per_cta; first < a.groups; first += (int64_t)gridDim.x * per_cta) {
+    const int64_t group = first + warp / a.split;
+    const int64_t r0 = min(group, a.groups - 1) * (16 * NP);
+    const uint8_t* q[2 * NP];
+    const uint16_t* s[2 * NP];
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i) {  // rows behind the last read it again
+      const int64_t n = min(r0 + 8 * i + g, a.N - 1);
+      q[i] = a.q + n * a.row_bytes + 16 * t4;
+      s[i] = a.s + n * a.row_scales;
+    }
+    float acc[NP][NT][4] = {};
+    for (int64_t k0 = 0; k0 < a.K; k0 += a.kc) {
+      const int kn = (int)min((int64_t)a.kc, a.K - k0);
+      const int nb = (int)w4_blocks(kn), pairs = (nb + 1) / 2;
+      const int64_t b0 = k0 / kW4Block, last = b0 + nb - 1;
+      MvTile<NP> cur, next;
+      const bool work = group < a.groups && part < pairs;
+      if (work) mv_load<F16, SHIFT, NP>(cur, a, q, s, b0 + 2 * part, last);
+      if (a.kc < a.K || first == (int64_t)blockIdx.x * per_cta) {
+        __syncthreads();  // every warp is done with the last chunk of x
+        // x, zeros up to whole blocks: 16 bytes a thread where the rows are aligned
+        const int64_t row_elems = (int64_t)nb * kW4Block;
+        const bool vec = ((reinterpret_cast<uintptr_t>(a.x) | (uint64_t)(2 * a.ldx)) & 15u) == 0 && kn % 8 == 0;
+        if (vec) {
+          const int cols = (int)(row_elems / 8);
+          for (int i = tid; i < a.T * cols; i += kMvThreads) {
+            const int t = i / cols, c = i - t * cols;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (8 * c < kn) v = ld_v4(a.x + t * a.ldx + k0 + 8 * c);
+            *reinterpret_cast<uint4*>(smem + (size_t)t * pitch + 16 * c) = v;
+          }
+        } else {
+          for (int64_t i = tid; i < a.T * row_elems; i += kMvThreads) {
+            const int t = (int)(i / row_elems), k = (int)(i - t * row_elems);
+            *reinterpret_cast<uint16_t*>(smem + (size_t)t * pitch + 2 * k) =
+                k < kn ? __ldg(a.x + t * a.ldx + k0 + k) : (uint16_t)0;
+          }
+        }
+        __syncthreads();
+      }
+      if (work)
+        for (int p = part; p < pairs; p += a.split) {
+          const bool more = p + a.split < pairs;
+          if (more) mv_load<F16, SHIFT, NP>(next, a, q, s, b0 + 2 * (p + a.split), last);
+          mv_block<F16, SHIFT, NT, NP>(cur.w[0], cur.s[0], xs + 512 * p, pitch, tok, acc);
+          if (2 * p + 1 < nb) mv_block<F16, SHIFT, NT, NP>(cur.w[1], cur.s[1], xs + 512 * p + 256, pitch, tok, acc);
+          if (more) cur = next;
+        }
+    }
+    if (a.split == 1) {
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = 8 * n + 2 * t4 + (i & 1);
+            const int64_t row = r0 + 16 * p + 8 * (i >> 1) + g;
+            if (group < a.groups && t < a.T && row < a.N) mv_store<F16>(a, t, row, acc[p][n][i]);
+          }
+    } else {
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float2*>(red + ((size_t)warp * 16 * NP + 16 * p + 8 * h + g) * (8 * NT) + 8 * n + 2 * t4) =
+                make_float2(acc[p][n][2 * h], acc[p][n][2 * h + 1]);
+      __syncthreads();
+      const int rows = per_cta * 16 * NP;
+      for (int o = tid; o < rows * a.T; o += kMvThreads) {
+        const int t = o / rows, r = o - t * rows, w0 = r / (16 * NP) * a.split;
+        const int64_t row = first * (16 * NP) + r;
+        if (row >= a.N) continue;
+        float v = 0.f;
+        for (int w = 0; w < a.split; ++w) v += red[((size_t)(w0 + w) * 16 * NP + r % (16 * NP)) * (8 * NT) + t];
+        mv_store<F16>(a, t, row, v);
+      }
+      __syncthreads();  // red is read
+    }
+  }
+}
+
+template <bool F16, int SHIFT>
+const void* mv_kernel(int nt, int np) {
+  if (nt == 1) return np == 1 ? (const void*)matvec_w4_kernel<F16, SHIFT, 1, 1> : (const void*)matvec_w4_kernel<F16, SHIFT, 1, 2>;
+  return np == 1 ? (const void*)matvec_w4_kernel<F16, SHIFT, 2, 1> : (const void*)matvec_w4_kernel<F16, SHIFT, 2, 2>;
 }
 
 }  // namespace
@@ -125,25 +206,27 @@ matvec_w4_kernel(const MvArgs a) {
 cudaError_t launch_matvec_w4(int T, int64_t N, int64_t K, int shift, const uint16_t* x, bool f16,
                              int64_t ldx, const uint8_t* q, const uint16_t* s, void* y, bool y_f32,
                              int64_t ldy, int sms, cudaStream_t st) {
-  MvArgs a{x, ldx, q, s, y, ldy, N, K, w4_row_bytes(K), w4_row_scales(K, 32 << shift), T, shift, 0, y_f32};
+  MvArgs a{x, ldx, q, s, y, ldy, N, K, 0, w4_row_bytes(K), w4_row_scales(K, 32 << shift), T, 0, 1, y_f32};
   const int nt = T > 8 ? 2 : 1;
-  const int64_t most = kMvXBytes / (2 * T) / kW4Block * kW4Block;
-  a.kc = (int)(w4_blocks(K) * kW4Block < most ? w4_blocks(K) * kW4Block : most);
-  int64_t grid = N < sms ? N : sms;
-  // a CTA keeps the sums of its rows in shared memory between K chunks
-  if (K > a.kc && grid < (N + kMvChunkRows - 1) / kMvChunkRows) grid = (N + kMvChunkRows - 1) / kMvChunkRows;
-  size_t smem = (size_t)T * (2 * a.kc + 64) + (size_t)kMvWarps * kMvRows * nt * 8 * sizeof(float);
-  if (K > a.kc) smem += (size_t)((N + grid - 1) / grid) * nt * 8 * sizeof(float);
-  if (smem > 227 * 1024) return cudaErrorInvalidValue;
-  const void* kernels[2][2] = {
-      {(const void*)matvec_w4_kernel<false, 1>, (const void*)matvec_w4_kernel<false, 2>},
-      {(const void*)matvec_w4_kernel<true, 1>, (const void*)matvec_w4_kernel<true, 2>}};
-  const void* fn = kernels[f16][nt - 1];
+  const int64_t most = kMvXBytes / (2 * T) / (2 * kW4Block) * (2 * kW4Block);  // whole pairs of blocks
+  a.kc = (int)std::min(w4_blocks(K) * kW4Block, most);
+  // 32 rows a group, 16 where that leaves SMs without one; and so many warps a group that the
+  // groups fill the device's warps once, at most one warp for two blocks
+  const int np = N > (int64_t)sms * 32 ? 2 : 1;
+  a.groups = (N + 16 * np - 1) / (16 * np);
+  const int pairs = (int)(w4_blocks(a.kc) + 1) / 2;
+  while (a.split < kMvWarps && a.split < pairs && a.groups * a.split * 2 <= (int64_t)sms * kMvWarps) a.split *= 2;
+  const int per_cta = kMvWarps / a.split;
+  const int64_t ctas = (a.groups + per_cta - 1) / per_cta;
+  const size_t smem = (size_t)T * (2 * a.kc + 64) + (a.split > 1 ? (size_t)kMvWarps * 16 * np * nt * 8 * sizeof(float) : 0);
+  const void* fn = f16 ? (shift == 0 ? mv_kernel<true, 0>(nt, np) : shift == 1 ? mv_kernel<true, 1>(nt, np) : mv_kernel<true, 2>(nt, np))
+                       : (shift == 0 ? mv_kernel<false, 0>(nt, np) : shift == 1 ? mv_kernel<false, 1>(nt, np) : mv_kernel<false, 2>(nt, np));
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e != cudaSuccess) return e;
   LaunchScope scope(MOE_K_OTHER, st);
   void* params[] = {&a};
-  e = cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(kMvThreads), params, smem, st);
+  const unsigned grid = (unsigned)std::min<int64_t>(ctas, sms);
+  e = cudaLaunchKernel(fn, dim3(grid), dim3(kMvThreads), params, smem, st);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

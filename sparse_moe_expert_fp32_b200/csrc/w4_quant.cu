@@ -5,14 +5,17 @@
 // Half a warp takes one storage block of 128 elements: lane 4 j + t reads elements
 // 32 j + 8 t .. + 7 (16 bytes, in row order) and writes word 4 t + j, so a block is one
 // 256-byte read and one 64-byte write, and a group's maximum is a shuffle over 4, 8 or 16
-// lanes. Bound by HBM: 2 bytes read and 1/2 + 2/group written per weight.
+// lanes. Four blocks a half warp are in flight. Bound by HBM: 2 bytes read and 1/2 + 2/group
+// written per weight.
 //
 // The quotient without a division: with 8-bit significands w / scale is either exactly half
-// way between two integers or at least 2^-10 away from it (for |w / scale| >= 1/2 its
-// distance is a nonzero multiple of 1/2 over twice an 8-bit integer). w times the rounded
-// reciprocal is within 2^-20 of it (|w / scale| <= 7.1), so rounding the product to a
-// multiple of 2^-12 first brings exact ties back and moves nothing else across a tie.
-// Scales so small that the reciprocal leaves fp32's range divide instead.
+// way between two integers or at least 2^-10 away from it (for |w / scale| >= 1/4 its
+// distance is a multiple of 1/2 over twice an 8-bit integer). fma(w, 1 / scale, 3072) is it
+// to a multiple of 2^-12, off by less than that, so an exact tie is exact again and nothing
+// else has crossed one; adding 2^23 + 2^22 + 8 - 3072 rounds it to an integer, ties to even, and
+// leaves code in the low bits. Scales so small that the reciprocal leaves fp32's range divide
+// instead. amax / 7 has no such ties (7 divides no odd multiple of a half step), so a
+// multiplication by 1/7 rounds to the same bf16.
 #include "moe_internal.h"
 #include "w4.cuh"
 
@@ -36,102 +39,165 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t e, int64_t K
   return v;
 }
 
-template <bool VEC>
+// Blocks i, i + stride, ... of a matrix with `per_row` blocks a row, without a division a step.
+struct BlockWalk {
+  int64_t row, b, per_row, row_step, b_step;
+  __device__ BlockWalk(int64_t i, int64_t stride, int64_t per_row)
+      : row(i / per_row), b(i % per_row), per_row(per_row), row_step(stride / per_row), b_step(stride % per_row) {}
+  __device__ void next() {
+    row += row_step;
+    b += b_step;
+    if (b >= per_row) {
+      b -= per_row;
+      ++row;
+    }
+  }
+};
+constexpr int kQuantBatch = 4;
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The word of eight elements' codes.
+__device__ __forceinline__ uint32_t codes8(const uint4& v, float s) {
+  float f[8];
+  unpack8(v, f);
+  uint32_t c[8];
+  if (s >= 0x1p-100f) {
+    const float inv = __frcp_rn(s);
+    const uint64_t inv2 = pack2(inv, inv), snap = pack2(3072.f, 3072.f), whole = pack2(12579848.f, 12579848.f);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const uint64_t r = add2(fma2(pack2(f[i], f[i + 1]), inv2, snap), whole);
+      c[i] = (uint32_t)r;
+      c[i + 1] = (uint32_t)(r >> 32);
+    }
+  } else {
+    const bool ok = s > 0.f;  // a zero or NaN scale: all codes 8
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      c[i] = ok ? (uint32_t)((int)fminf(fmaxf(rintf(__fdiv_rn(f[i], s)), -8.f), 7.f) + 8) : 8u;
+  }
+  // low bytes of the even elements, then of the odd ones; two nibbles a byte
+  const uint32_t e = __byte_perm(__byte_perm(c[0], c[2], 0x0040), __byte_perm(c[4], c[6], 0x0040), 0x5410);
+  const uint32_t o = __byte_perm(__byte_perm(c[1], c[3], 0x0040), __byte_perm(c[5], c[7], 0x0040), 0x5410);
+  return __byte_perm(e | (e >> 4), o | (o >> 4), 0x6420);
+}
+
+template <bool VEC, int SHIFT>
 __global__ void __launch_bounds__(kQuantThreads)
-quantize_w4_kernel(const uint16_t* __restrict__ w, int64_t rows, int64_t K, int shift,
-                   uint8_t* __restrict__ q, uint16_t* __restrict__ scales) {
+quantize_w4_kernel(const uint16_t* __restrict__ w, int64_t rows, int64_t K, uint8_t* __restrict__ q,
+                   uint16_t* __restrict__ scales) {
   const int lane = threadIdx.x & 15, j = lane >> 2, t = lane & 3;
   const int64_t blocks = w4_blocks(K);
-  const int64_t ns = w4_row_scales(K, 32 << shift);
-  const int64_t vblocks = (ns << shift) >> 2;  // blocks with the scale padding's share, >= blocks
-  const int64_t total = rows * vblocks;
+  const int64_t ns = w4_row_scales(K, 32 << SHIFT);
+  const int64_t vblocks = (ns << SHIFT) >> 2;  // blocks with the scale padding's share, >= blocks
   const int64_t stride = (int64_t)gridDim.x * (kQuantThreads / 16);
-  const int lanes = 4 << shift;  // lanes of a group
-  // every lane of a warp stays in the loop as long as one half has a block (the shuffles)
-  for (int64_t v0 = (int64_t)blockIdx.x * (kQuantThreads / 16) + ((threadIdx.x >> 5) << 1); v0 < total;
-       v0 += stride) {
-    const int64_t vb = v0 + ((threadIdx.x >> 4) & 1);
-    const bool in = vb < total;
-    const int64_t row = in ? vb / vblocks : 0, b = in ? vb - row * vblocks : 0;
-    const bool real = in && b < blocks;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (real) v = load8<VEC>(w + row * K, b * kW4Block + 32 * j + 8 * t, K);
-    // |w| as integers: infinities and NaN sort above every finite value
-    uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                          __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-    m = max(m & 0xffffu, m >> 16);
-    for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    // a group with an infinity or a NaN gets a NaN scale, so that all of it reads back as NaN
-    const uint16_t sb = m >= 0x7f80u ? (uint16_t)0x7fc0u
-                                     : f32_to_bf16_rn(__fdiv_rn(__uint_as_float(m << 16), 7.f));
-    const float s = __uint_as_float((uint32_t)sb << 16);
-    const int64_t g = (b * 4 + j) >> shift;
-    // a group has one writer: its first lane
-    if (in && (lane & (lanes - 1)) == 0) scales[row * ns + g] = sb;
-    if (!real) continue;
-    const bool ok = s > 0.f, tiny = s < 0x1p-100f;
-    const float inv = ok ? __frcp_rn(s) : 0.f;
-    float f[8];
-    unpack8(v, f);
-    uint32_t word = 0;
+  constexpr int lanes = 4 << SHIFT;  // lanes of a group
+  BlockWalk at((int64_t)blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4), stride, vblocks);
+  // both halves of a warp stay in the loop as long as one has a block (the shuffles)
+  while (__any_sync(0xffffffffu, at.row < rows)) {
+    uint4 v[kQuantBatch];
+    int64_t row[kQuantBatch], b[kQuantBatch];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float r = 0.f;
-      if (ok) {
-        const float p = tiny ? __fdiv_rn(f[i], s) : f[i] * inv;
-        // round to a multiple of 2^-12 (1.5 * 2^11 has that ulp), then to an integer
-        const float snapped = __fadd_rn(__fadd_rn(p, 0x1.8p11f), -0x1.8p11f);
-        r = fminf(fmaxf(rintf(snapped), -8.f), 7.f);
-      }
-      word |= (uint32_t)((int)r + 8) << (4 * ((i >> 1) + 4 * (i & 1)));
+    for (int u = 0; u < kQuantBatch; ++u) {
+      row[u] = at.row;
+      b[u] = at.b;
+      v[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (at.row < rows && at.b < blocks) v[u] = load8<VEC>(w + at.row * K, at.b * kW4Block + 32 * j + 8 * t, K);
+      at.next();
     }
-    *reinterpret_cast<uint32_t*>(q + (row * blocks + b) * kW4BlockBytes + 16 * t + 4 * j) = word;
+#pragma unroll
+    for (int u = 0; u < kQuantBatch; ++u) {
+      // |w| as integers: infinities and NaN sort above every finite value
+      uint32_t m = __vmaxu2(__vmaxu2(v[u].x & 0x7fff7fffu, v[u].y & 0x7fff7fffu),
+                            __vmaxu2(v[u].z & 0x7fff7fffu, v[u].w & 0x7fff7fffu));
+      m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+      for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      // a group with an infinity or a NaN gets a NaN scale, so that all of it reads back as NaN
+      const uint16_t sb =
+          m >= 0x7f80u ? (uint16_t)0x7fc0u : f32_to_bf16_rn(__uint_as_float(m << 16) * (1.f / 7.f));
+      if (row[u] >= rows) continue;
+      // a group has one writer: its first lane
+      if ((lane & (lanes - 1)) == 0) scales[row[u] * ns + ((b[u] * 4 + j) >> SHIFT)] = sb;
+      if (b[u] < blocks)
+        *reinterpret_cast<uint32_t*>(q + (row[u] * blocks + b[u]) * kW4BlockBytes + 16 * t + 4 * j) =
+            codes8(v[u], __uint_as_float((uint32_t)sb << 16));
+    }
   }
 }
 
 // The inverse: (c - 8) s is exact in fp32 (4 by 8 significant bits); bf16 rounds it once.
-template <bool VEC, bool BF16>
+template <bool VEC, bool BF16, int SHIFT>
 __global__ void __launch_bounds__(kQuantThreads)
 dequantize_w4_kernel(const uint8_t* __restrict__ q, const uint16_t* __restrict__ scales,
-                     int64_t rows, int64_t K, int shift, void* __restrict__ out) {
+                     int64_t rows, int64_t K, void* __restrict__ out) {
   const int lane = threadIdx.x & 15, j = lane >> 2, t = lane & 3;
   const int64_t blocks = w4_blocks(K);
-  const int64_t ns = w4_row_scales(K, 32 << shift);
-  const int64_t total = rows * blocks, stride = (int64_t)gridDim.x * (kQuantThreads / 16);
-  for (int64_t vb = (int64_t)blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4); vb < total;
-       vb += stride) {
-    const int64_t row = vb / blocks, b = vb - row * blocks;
-    const int64_t e = b * kW4Block + 32 * j + 8 * t;
-    if (e >= K) continue;
-    const uint32_t word =
-        __ldg(reinterpret_cast<const uint32_t*>(q + vb * kW4BlockBytes + 16 * t + 4 * j));
-    const float s = bf16lo(__ldg(scales + row * ns + ((b * 4 + j) >> shift)));
-    float f[8];
+  const int64_t ns = w4_row_scales(K, 32 << SHIFT);
+  const int64_t stride = (int64_t)gridDim.x * (kQuantThreads / 16);
+  BlockWalk at((int64_t)blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4), stride, blocks);
+  while (at.row < rows) {
+    uint32_t word[kQuantBatch], scale[kQuantBatch];
+    int64_t row[kQuantBatch], first[kQuantBatch];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      f[i] = (float)((int)((word >> (4 * ((i >> 1) + 4 * (i & 1)))) & 15u) - 8) * s;
-    if constexpr (BF16) {
-      uint16_t* o = static_cast<uint16_t*>(out) + row * K + e;
-      if constexpr (VEC) {
-        uint32_t u[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          u[i] = (uint32_t)f32_to_bf16_rn(f[2 * i]) | (uint32_t)f32_to_bf16_rn(f[2 * i + 1]) << 16;
-        *reinterpret_cast<uint4*>(o) = make_uint4(u[0], u[1], u[2], u[3]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (e + i < K) o[i] = f32_to_bf16_rn(f[i]);
+    for (int u = 0; u < kQuantBatch; ++u) {
+      row[u] = at.row;
+      first[u] = at.b * kW4Block + 32 * j + 8 * t;
+      word[u] = scale[u] = 0u;
+      if (at.row < rows && first[u] < K) {
+        word[u] = __ldg(reinterpret_cast<const uint32_t*>(q + (at.row * blocks + at.b) * kW4BlockBytes + 16 * t + 4 * j));
+        scale[u] = __ldg(scales + at.row * ns + ((at.b * 4 + j) >> SHIFT));
       }
-    } else {
-      float* o = static_cast<float*>(out) + row * K + e;
-      if constexpr (VEC) {
-        reinterpret_cast<float4*>(o)[0] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4*>(o)[1] = make_float4(f[4], f[5], f[6], f[7]);
-      } else {
+      at.next();
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (e + i < K) o[i] = f[i];
+    for (int u = 0; u < kQuantBatch; ++u) {
+      if (row[u] >= rows || first[u] >= K) continue;
+      const uint4 c = w4_pairs<false>(word[u]);  // c - 8 as bf16, exactly
+      const int64_t e = row[u] * K + first[u];
+      const int n = (int)min((int64_t)8, K - first[u]);
+      if constexpr (BF16) {
+        uint16_t* o = static_cast<uint16_t*>(out) + e;
+        const uint32_t s2 = scale[u] * 0x10001u;
+        const uint4 r = make_uint4(mul_bf16x2(c.x, s2), mul_bf16x2(c.y, s2), mul_bf16x2(c.z, s2), mul_bf16x2(c.w, s2));
+        if constexpr (VEC) {
+          *reinterpret_cast<uint4*>(o) = r;
+        } else {
+          const uint32_t p[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < n) o[i] = (uint16_t)(p[i / 2] >> (16 * (i & 1)));
+        }
+      } else {
+        float* o = static_cast<float*>(out) + e;
+        const float s = bf16lo(scale[u]);
+        float f[8];
+        unpack8(c, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= s;
+        if constexpr (VEC) {
+          reinterpret_cast<float4*>(o)[0] = make_float4(f[0], f[1], f[2], f[3]);
+          reinterpret_cast<float4*>(o)[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < n) o[i] = f[i];
+        }
       }
     }
   }
@@ -150,12 +216,31 @@ cudaError_t launch_quantize_w4(const uint16_t* w, int64_t rows, int64_t K, int s
   const int64_t items = rows * ((w4_row_scales(K, 32 << shift) << shift) >> 2);
   if (items == 0) return cudaSuccess;
   LaunchScope scope(MOE_K_OTHER, st);
-  if (K % 8 == 0)
-    quantize_w4_kernel<true><<<quant_blocks(items, sms), kQuantThreads, 0, st>>>(w, rows, K, shift, q, scales);
-  else
-    quantize_w4_kernel<false><<<quant_blocks(items, sms), kQuantThreads, 0, st>>>(w, rows, K, shift, q, scales);
+  const int grid = quant_blocks(items, sms);
+#define MOE_QUANT(VEC, SH) \
+  quantize_w4_kernel<VEC, SH><<<grid, kQuantThreads, 0, st>>>(w, rows, K, q, scales)
+  if (K % 8 == 0) {
+    if (shift == 0) MOE_QUANT(true, 0);
+    else if (shift == 1) MOE_QUANT(true, 1);
+    else MOE_QUANT(true, 2);
+  } else {
+    if (shift == 0) MOE_QUANT(false, 0);
+    else if (shift == 1) MOE_QUANT(false, 1);
+    else MOE_QUANT(false, 2);
+  }
+#undef MOE_QUANT
   return cudaGetLastError();
 }
+
+namespace {
+template <bool VEC, bool BF16>
+void dequantize(const uint8_t* q, const uint16_t* scales, int64_t rows, int64_t K, int shift, void* out, int grid,
+                cudaStream_t st) {
+  if (shift == 0) dequantize_w4_kernel<VEC, BF16, 0><<<grid, kQuantThreads, 0, st>>>(q, scales, rows, K, out);
+  else if (shift == 1) dequantize_w4_kernel<VEC, BF16, 1><<<grid, kQuantThreads, 0, st>>>(q, scales, rows, K, out);
+  else dequantize_w4_kernel<VEC, BF16, 2><<<grid, kQuantThreads, 0, st>>>(q, scales, rows, K, out);
+}
+}  // namespace
 
 cudaError_t launch_dequantize_w4(const uint8_t* q, const uint16_t* scales, int64_t rows, int64_t K,
                                  int shift, void* out, bool bf16, int sms, cudaStream_t st) {
@@ -163,16 +248,13 @@ cudaError_t launch_dequantize_w4(const uint8_t* q, const uint16_t* scales, int64
   if (items == 0) return cudaSuccess;
   LaunchScope scope(MOE_K_OTHER, st);
   const int grid = quant_blocks(items, sms);
-#define MOE_DEQ(VEC, BF) \
-  dequantize_w4_kernel<VEC, BF><<<grid, kQuantThreads, 0, st>>>(q, scales, rows, K, shift, out)
   if (K % 8 == 0) {
-    if (bf16) MOE_DEQ(true, true);
-    else MOE_DEQ(true, false);
+    if (bf16) dequantize<true, true>(q, scales, rows, K, shift, out, grid, st);
+    else dequantize<true, false>(q, scales, rows, K, shift, out, grid, st);
   } else {
-    if (bf16) MOE_DEQ(false, true);
-    else MOE_DEQ(false, false);
+    if (bf16) dequantize<false, true>(q, scales, rows, K, shift, out, grid, st);
+    else dequantize<false, false>(q, scales, rows, K, shift, out, grid, st);
   }
-#undef MOE_DEQ
   return cudaGetLastError();
 }
 
