@@ -310,71 +310,91 @@ def moe_layer_forward_fp8(shape, x, weights, experts, out, ws, topk_ids=None, to
 
 # The few-token and 4-bit calls check their tensors against the shapes they stand for: a tensor
 # of another type, device, layout or size is refused before anything is enqueued. Addresses
-# (ints) pass unchecked, as everywhere.
+# (ints) pass unchecked, as everywhere. These calls can be shorter than the host's work for
+# them, so that work is kept small.
 
-def _need(where: str, t, dtype: str, numel: int, optional: bool = False) -> Optional[int]:
-    """Address of a dense device tensor of `dtype` with at least `numel` elements."""
-    if t is None:
-        if optional:
-            return None
-        raise MoeError(MOE_ERR_INVALID_ARG, where)
+class _Torch:
+    """torch, imported at the first such call, with what the checks need of it at hand."""
+
+    def __getattr__(self, name):
+        import torch
+
+        self.bf16, self.f16, self.f32 = torch.bfloat16, torch.float16, torch.float32
+        self.i32, self.u8 = torch.int32, torch.uint8
+        self.device = torch.cuda.current_device
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.stream = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+        return self.__dict__[name]
+
+
+_T = _Torch()
+
+
+def _need(where: str, t, dtype, numel: int, dev: int) -> Optional[int]:
+    """Address of a dense tensor of `dtype` on device `dev` with at least `numel` elements."""
     if isinstance(t, int):
         return t
-    import torch
-
-    if (t.dtype is not getattr(torch, dtype) or not t.is_cuda or t.numel() < numel
-            or t.get_device() != torch.cuda.current_device() or not t.is_contiguous()):
+    if (t is None or t.dtype is not dtype or t.get_device() != dev or t.numel() < numel
+            or not t.is_contiguous()):
         raise MoeError(MOE_ERR_INVALID_ARG, where)
     return t.data_ptr()
 
 
-def _few_args(where, s, x, weights, out, ws, topk_ids, topk_w, gap, routed):
-    """(x, moe_weights, out, topk_ids, topk_w, gap) of a few-token call."""
-    T, H, E = max(s.T, 0), s.H, s.E
-    if not isinstance(weights, moe_weights):
-        w = weights
-        weights = moe_weights(
-            _need(where, w["w_router"], "float32", E * H),
-            _need(where, w.get("router_bias"), "float32", E, True),
-            _need(where, w["w_gate_up"], "bfloat16", E * 2 * s.I * H) if routed else None,
-            _need(where, w["w_down"], "bfloat16", E * H * s.I) if routed else None,
-            _need(where, w["ws_gate_up"], "bfloat16", 2 * s.Is * H),
-            _need(where, w["ws_down"], "bfloat16", H * s.Is),
-            _need(where, w["w_shared_gate"], "bfloat16", H), None, None)
-    return (_need(where, x, "bfloat16", T * H), weights, _need(where, out, "float32", T * H),
-            _need(where, topk_ids, "int32", T * s.k, True),
-            _need(where, topk_w, "float32", T * s.k, True), _need(where, gap, "float32", T, True),
-            _need(where, ws, "uint8", 0))
+def _device(t) -> int:
+    """The current device, as far as a tensor can be on one (the CPU-only checks see -2)."""
+    return _T.device() if t is None or isinstance(t, int) or t.is_cuda else -2
+
+
+def _few_stream(stream, dev: int) -> Optional[int]:
+    return _T.stream(dev) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _few(f, s, x, weights, experts, out, ws, topk_ids, topk_w, gap, stream):
+    T, H, E, I, Is = max(s.T, 0), s.H, s.E, s.I, s.Is
+    dev, w = _device(x), weights
+    bf, f32 = _T.bf16, _T.f32
+    if not isinstance(w, moe_weights):
+        bias = w.get("router_bias")
+        w = moe_weights(
+            _need(f, w["w_router"], f32, E * H, dev),
+            None if bias is None else _need(f, bias, f32, E, dev),
+            _need(f, w["w_gate_up"], bf, E * 2 * I * H, dev) if experts is None else None,
+            _need(f, w["w_down"], bf, E * H * I, dev) if experts is None else None,
+            _need(f, w["ws_gate_up"], bf, 2 * Is * H, dev), _need(f, w["ws_down"], bf, H * Is, dev),
+            _need(f, w["w_shared_gate"], bf, H, dev), None, None)
+    if experts is not None and not isinstance(experts, moe_w4_experts):
+        g, q = int(experts["group"]), experts
+        experts = moe_w4_experts(
+            _need(f, q["q_gate_up"], _T.u8, E * 2 * I * _lib.moe_w4_row_bytes(H), dev),
+            _need(f, q["s_gate_up"], bf, E * 2 * I * _lib.moe_w4_row_scales(H, g), dev),
+            _need(f, q["q_down"], _T.u8, E * H * _lib.moe_w4_row_bytes(I), dev),
+            _need(f, q["s_down"], bf, E * H * _lib.moe_w4_row_scales(I, g), dev), g)
+    ids = None if topk_ids is None else _need(f, topk_ids, _T.i32, T * s.k, dev)
+    p = None if topk_w is None else _need(f, topk_w, f32, T * s.k, dev)
+    gap = None if gap is None else _need(f, gap, f32, T, dev)
+    head = (ctypes.byref(s), _need(f, x, bf, T * H, dev), ctypes.byref(w))
+    tail = (_need(f, out, f32, T * H, dev), ids, p, gap, _need(f, ws, _T.u8, 0, dev), _nbytes(ws),
+            _few_stream(stream, dev))
+    if experts is None:
+        _check(_lib.moe_layer_forward_few(*head, *tail), f)
+    else:
+        _check(_lib.moe_layer_forward_few_w4(*head, ctypes.byref(experts), *tail), f)
 
 
 def moe_layer_forward_few(shape, x, weights, out, ws, topk_ids=None, topk_w=None, gap=None,
                           stream=None):
     """The whole layer for T <= 8 tokens in one kernel (T * H <= 65536)."""
-    f = "moe_layer_forward_few"
-    x, w, out, topk_ids, topk_w, gap, wp = _few_args(f, shape, x, weights, out, ws, topk_ids,
-                                                     topk_w, gap, True)
-    _check(_lib.moe_layer_forward_few(ctypes.byref(shape), x, ctypes.byref(w), out, topk_ids,
-                                      topk_w, gap, wp, _nbytes(ws), _stream(stream)), f)
+    _few("moe_layer_forward_few", shape, x, weights, None, out, ws, topk_ids, topk_w, gap, stream)
 
 
 def moe_layer_forward_few_w4(shape, x, weights, experts, out, ws, topk_ids=None, topk_w=None,
                              gap=None, stream=None):
     """moe_layer_forward_few with the routed experts in 4-bit groups: `experts` is a
     moe_w4_experts or a dict as quantize_w4_experts returns it."""
-    f = "moe_layer_forward_few_w4"
-    s = shape
-    if not isinstance(experts, moe_w4_experts):
-        g, E, H, I = int(experts["group"]), s.E, s.H, s.I
-        experts = moe_w4_experts(
-            _need(f, experts["q_gate_up"], "uint8", E * 2 * I * _lib.moe_w4_row_bytes(H)),
-            _need(f, experts["s_gate_up"], "bfloat16", E * 2 * I * _lib.moe_w4_row_scales(H, g)),
-            _need(f, experts["q_down"], "uint8", E * H * _lib.moe_w4_row_bytes(I)),
-            _need(f, experts["s_down"], "bfloat16", E * H * _lib.moe_w4_row_scales(I, g)), g)
-    x, w, out, topk_ids, topk_w, gap, wp = _few_args(f, s, x, weights, out, ws, topk_ids, topk_w,
-                                                     gap, False)
-    _check(_lib.moe_layer_forward_few_w4(ctypes.byref(s), x, ctypes.byref(w), ctypes.byref(experts),
-                                         out, topk_ids, topk_w, gap, wp, _nbytes(ws),
-                                         _stream(stream)), f)
+    if experts is None:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_layer_forward_few_w4")
+    _few("moe_layer_forward_few_w4", shape, x, weights, experts, out, ws, topk_ids, topk_w, gap,
+         stream)
 
 
 def moe_w4_row_bytes(K: int) -> int:
@@ -402,58 +422,50 @@ def _rows(where, t, dtypes):
 
 def moe_quantize_w4(w, q, s, group, stream=None) -> None:
     """w bf16 [..., K] -> codes q uint8 [..., row bytes] and scales s bf16 [..., row scales]."""
-    import torch
-
-    f = "moe_quantize_w4"
-    rows, K = _rows(f, w, (torch.bfloat16,))
+    f, dev, group = "moe_quantize_w4", _device(w), int(group)
+    rows, K = _rows(f, w, (_T.bf16,))
     _check(_lib.moe_quantize_w4(
-        rows, K, int(group), _need(f, w, "bfloat16", 0),
-        _need(f, q, "uint8", rows * _lib.moe_w4_row_bytes(K)),
-        _need(f, s, "bfloat16", rows * _lib.moe_w4_row_scales(K, int(group))), _stream(stream)), f)
+        rows, K, group, _need(f, w, _T.bf16, 0, dev),
+        _need(f, q, _T.u8, rows * _lib.moe_w4_row_bytes(K), dev),
+        _need(f, s, _T.bf16, rows * _lib.moe_w4_row_scales(K, group), dev),
+        _few_stream(stream, dev)), f)
 
 
 def moe_dequantize_w4(q, s, w, group, stream=None) -> None:
     """The inverse into w, fp32 or bf16 [..., K]."""
-    import torch
-
-    f = "moe_dequantize_w4"
-    rows, K = _rows(f, w, (torch.float32, torch.bfloat16))
-    bf16 = w.dtype is torch.bfloat16
+    f, dev, group = "moe_dequantize_w4", _device(w), int(group)
+    rows, K = _rows(f, w, (_T.f32, _T.bf16))
     _check(_lib.moe_dequantize_w4(
-        rows, K, int(group), _need(f, q, "uint8", rows * _lib.moe_w4_row_bytes(K)),
-        _need(f, s, "bfloat16", rows * _lib.moe_w4_row_scales(K, int(group))),
-        MOE_BF16 if bf16 else MOE_F32, _need(f, w, "bfloat16" if bf16 else "float32", 0),
-        _stream(stream)), f)
+        rows, K, group, _need(f, q, _T.u8, rows * _lib.moe_w4_row_bytes(K), dev),
+        _need(f, s, _T.bf16, rows * _lib.moe_w4_row_scales(K, group), dev),
+        MOE_BF16 if w.dtype is _T.bf16 else MOE_F32, _need(f, w, w.dtype, 0, dev),
+        _few_stream(stream, dev)), f)
 
 
-def _strided(where, t, dtype):
+def _strided(where, t, dtype, dev):
     """(address, row stride) of a device matrix whose rows are dense."""
-    import torch
-
     T, n = t.shape
-    if (t.dtype is not dtype or not t.is_cuda or t.get_device() != torch.cuda.current_device()
-            or (n > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) < n)):
+    ld, one = t.stride()
+    if t.dtype is not dtype or t.get_device() != dev or (n > 1 and one != 1) or (T > 1 and ld < n):
         raise MoeError(MOE_ERR_INVALID_ARG, where)
-    return t.data_ptr(), max(t.stride(0), n)
+    return t.data_ptr(), max(ld, n)
 
 
 def moe_matvec_w4(x, q, s, y, group, stream=None) -> None:
     """y [T, N] = x [T, K] W^T for T <= 16, W [N, K] as moe_quantize_w4 stores it. x is bf16 or
     fp16, y is fp32 or x's type; the rows of both may have a stride."""
-    import torch
-
-    f = "moe_matvec_w4"
+    f, dev, group = "moe_matvec_w4", _device(x), int(group)
     if x.dim() != 2 or y.dim() != 2 or x.shape[0] != y.shape[0]:
         raise MoeError(MOE_ERR_INVALID_ARG, f)
     (T, K), N = x.shape, y.shape[1]
-    xt = MOE_F16 if x.dtype is torch.float16 else MOE_BF16
-    yt = MOE_F32 if y.dtype is torch.float32 else xt
-    xp, ldx = _strided(f, x, torch.float16 if xt == MOE_F16 else torch.bfloat16)
-    yp, ldy = _strided(f, y, y.dtype if yt == MOE_F32 else x.dtype)
+    half, f32 = x.dtype is _T.f16, y.dtype is _T.f32
+    xp, ldx = _strided(f, x, _T.f16 if half else _T.bf16, dev)
+    yp, ldy = _strided(f, y, _T.f32 if f32 else x.dtype, dev)
+    xt = MOE_F16 if half else MOE_BF16
     _check(_lib.moe_matvec_w4(
-        T, N, K, int(group), xt, xp, ldx, _need(f, q, "uint8", N * _lib.moe_w4_row_bytes(K)),
-        _need(f, s, "bfloat16", N * _lib.moe_w4_row_scales(K, int(group))), yt, yp, ldy,
-        _stream(stream)), f)
+        T, N, K, group, xt, xp, ldx, _need(f, q, _T.u8, N * _lib.moe_w4_row_bytes(K), dev),
+        _need(f, s, _T.bf16, N * _lib.moe_w4_row_scales(K, group), dev), MOE_F32 if f32 else xt, yp,
+        ldy, _few_stream(stream, dev)), f)
 
 
 def _ws_args(ws):

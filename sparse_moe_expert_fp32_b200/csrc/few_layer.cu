@@ -1337,7 +1337,8 @@ cudaError_t launch_few_layer(const moe_shape& s, const Layout& L, char* ws, cons
                    : a.shift == 0 ? (const void*)few_layer_kernel<0>
                    : a.shift == 1 ? (const void*)few_layer_kernel<1>
                                   : (const void*)few_layer_kernel<2>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSmem);
+  static std::atomic<uint64_t> done[4];
+  cudaError_t e = allow_smem(fn, kFewSmem, done[q ? a.shift : 3]);
   if (e != cudaSuccess) return e;
   LaunchScope scope(MOE_K_OTHER, st);
   void* params[] = {&a, &m};

@@ -113,6 +113,17 @@ LaunchScope::LaunchScope(moe_kernel id, cudaStream_t s, int nkernels) : slot(-1)
   g_recs.push_back({(int)id, a, b});
 }
 
+cudaError_t allow_smem(const void* fn, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 LaunchScope::~LaunchScope() {
   nvtxRangePop();
   if (slot < 0) return;

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "moe.h"
 
 namespace moe {
@@ -127,6 +129,10 @@ struct LaunchScope {
   int slot;
   cudaStream_t stream;
 };
+
+// Raises a kernel's dynamic shared memory limit, once per kernel and device: `done` is the
+// kernel's own bit set of devices.
+cudaError_t allow_smem(const void* fn, size_t bytes, std::atomic<uint64_t>& done);
 
 // ---------------------------------------------------------------- kernel launches
 // Every launcher enqueues on `st` and returns cudaGetLastError().

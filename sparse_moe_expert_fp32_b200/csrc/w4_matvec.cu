@@ -6,7 +6,7 @@
 // MMA operands of them. A group of warps takes 32 matrix rows (16 if there are few) and splits
 // their 128-element blocks; the fewer rows there are, the more warps a group has, so that small
 // matrices still spread over all SMs without a second launch. The codes are loaded straight to
-// registers, two blocks (128 bytes a row) ahead; x is staged in shared memory. The MMA's A is 16
+// registers, a block ahead; x is staged in shared memory. The MMA's A is 16
 // matrix rows, made in registers, its columns are 8 rows of x. The codes enter as exact
 // integers; the fp32 sum over a scale group is multiplied by the scale and added to the running
 // fp32 sums, so no product or weight is rounded.
@@ -36,24 +36,21 @@ struct MvArgs {
   int T, kc, split, y_f32;  // split: warps of a row group
 };
 
-// Two blocks of 16 NP rows: row[i] is this lane's row 8 i + g.
+// A block of 16 NP rows: this lane's rows 8 i + g.
 template <int NP>
 struct MvTile {
-  uint4 w[2][2 * NP];
-  uint2 s[2][2 * NP];
+  uint4 w[2 * NP];
+  uint2 s[2 * NP];
 };
 
-template <bool F16, int SHIFT, int NP>
-__device__ __forceinline__ void mv_load(MvTile<NP>& m, const MvArgs& a, const uint8_t* const (&q)[2 * NP],
-                                        const uint16_t* const (&s)[2 * NP], int64_t b, int64_t last) {
+template <int SHIFT, int NP>
+__device__ __forceinline__ void mv_load(MvTile<NP>& m, const uint8_t* q, const uint16_t* s, const int (&row)[2 * NP],
+                                        int64_t row_bytes, int64_t row_scales, int64_t b) {
 #pragma unroll
-  for (int i = 0; i < 2 * NP; ++i)
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int64_t bu = min(b + u, last);
-      m.w[u][i] = ld_stream_v4(q[i] + bu * kW4BlockBytes);
-      m.s[u][i] = w4_block_scales(s[i], (int)bu, SHIFT);
-    }
+  for (int i = 0; i < 2 * NP; ++i) {
+    m.w[i] = ld_stream_v4(q + row[i] * row_bytes + b * kW4BlockBytes);
+    m.s[i] = w4_block_scales(s + row[i] * row_scales, (int)b, SHIFT);
+  }
 }
 
 template <bool F16, int SHIFT, int NT, int NP>
@@ -113,22 +110,19 @@ matvec_w4_kernel(const MvArgs a) {
   for (int64_t first = (int64_t)blockIdx.x * per_cta; first < a.groups; first += (int64_t)gridDim.x * per_cta) {
     const int64_t group = first + warp / a.split;
     const int64_t r0 = min(group, a.groups - 1) * (16 * NP);
-    const uint8_t* q[2 * NP];
-    const uint16_t* s[2 * NP];
+    const uint8_t* q = a.q + r0 * a.row_bytes + 16 * t4;
+    const uint16_t* s = a.s + r0 * a.row_scales;
+    int row[2 * NP];  // rows behind the last read it again
 #pragma unroll
-    for (int i = 0; i < 2 * NP; ++i) {  // rows behind the last read it again
-      const int64_t n = min(r0 + 8 * i + g, a.N - 1);
-      q[i] = a.q + n * a.row_bytes + 16 * t4;
-      s[i] = a.s + n * a.row_scales;
-    }
+    for (int i = 0; i < 2 * NP; ++i) row[i] = (int)min((int64_t)(8 * i + g), a.N - 1 - r0);
     float acc[NP][NT][4] = {};
     for (int64_t k0 = 0; k0 < a.K; k0 += a.kc) {
       const int kn = (int)min((int64_t)a.kc, a.K - k0);
-      const int nb = (int)w4_blocks(kn), pairs = (nb + 1) / 2;
-      const int64_t b0 = k0 / kW4Block, last = b0 + nb - 1;
+      const int nb = (int)w4_blocks(kn);
+      const int64_t b0 = k0 / kW4Block;
       MvTile<NP> cur, next;
-      const bool work = group < a.groups && part < pairs;
-      if (work) mv_load<F16, SHIFT, NP>(cur, a, q, s, b0 + 2 * part, last);
+      const bool work = group < a.groups && part < nb;
+      if (work) mv_load<SHIFT, NP>(cur, q, s, row, a.row_bytes, a.row_scales, b0 + part);
       if (a.kc < a.K || first == (int64_t)blockIdx.x * per_cta) {
         __syncthreads();  // every warp is done with the last chunk of x
         // x, zeros up to whole blocks: 16 bytes a thread where the rows are aligned
@@ -152,11 +146,10 @@ matvec_w4_kernel(const MvArgs a) {
         __syncthreads();
       }
       if (work)
-        for (int p = part; p < pairs; p += a.split) {
-          const bool more = p + a.split < pairs;
-          if (more) mv_load<F16, SHIFT, NP>(next, a, q, s, b0 + 2 * (p + a.split), last);
-          mv_block<F16, SHIFT, NT, NP>(cur.w[0], cur.s[0], xs + 512 * p, pitch, tok, acc);
-          if (2 * p + 1 < nb) mv_block<F16, SHIFT, NT, NP>(cur.w[1], cur.s[1], xs + 512 * p + 256, pitch, tok, acc);
+        for (int b = part; b < nb; b += a.split) {
+          const bool more = b + a.split < nb;
+          if (more) mv_load<SHIFT, NP>(next, q, s, row, a.row_bytes, a.row_scales, b0 + b + a.split);
+          mv_block<F16, SHIFT, NT, NP>(cur.w, cur.s, xs + 256 * b, pitch, tok, acc);
           if (more) cur = next;
         }
     }
@@ -208,20 +201,21 @@ cudaError_t launch_matvec_w4(int T, int64_t N, int64_t K, int shift, const uint1
                              int64_t ldy, int sms, cudaStream_t st) {
   MvArgs a{x, ldx, q, s, y, ldy, N, K, 0, w4_row_bytes(K), w4_row_scales(K, 32 << shift), T, 0, 1, y_f32};
   const int nt = T > 8 ? 2 : 1;
-  const int64_t most = kMvXBytes / (2 * T) / (2 * kW4Block) * (2 * kW4Block);  // whole pairs of blocks
+  const int64_t most = kMvXBytes / (2 * T) / kW4Block * kW4Block;
   a.kc = (int)std::min(w4_blocks(K) * kW4Block, most);
   // 32 rows a group, 16 where that leaves SMs without one; and so many warps a group that the
-  // groups fill the device's warps once, at most one warp for two blocks
+  // groups fill the device's warps once, at most one warp for a block
   const int np = N > (int64_t)sms * 32 ? 2 : 1;
   a.groups = (N + 16 * np - 1) / (16 * np);
-  const int pairs = (int)(w4_blocks(a.kc) + 1) / 2;
-  while (a.split < kMvWarps && a.split < pairs && a.groups * a.split * 2 <= (int64_t)sms * kMvWarps) a.split *= 2;
+  const int nb = (int)w4_blocks(a.kc);
+  while (a.split < kMvWarps && a.split < nb && a.groups * a.split * 2 <= (int64_t)sms * kMvWarps) a.split *= 2;
   const int per_cta = kMvWarps / a.split;
   const int64_t ctas = (a.groups + per_cta - 1) / per_cta;
   const size_t smem = (size_t)T * (2 * a.kc + 64) + (a.split > 1 ? (size_t)kMvWarps * 16 * np * nt * 8 * sizeof(float) : 0);
   const void* fn = f16 ? (shift == 0 ? mv_kernel<true, 0>(nt, np) : shift == 1 ? mv_kernel<true, 1>(nt, np) : mv_kernel<true, 2>(nt, np))
                        : (shift == 0 ? mv_kernel<false, 0>(nt, np) : shift == 1 ? mv_kernel<false, 1>(nt, np) : mv_kernel<false, 2>(nt, np));
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  static std::atomic<uint64_t> done[2][3][2][2];
+  cudaError_t e = allow_smem(fn, 227 * 1024, done[f16][shift][nt - 1][np - 1]);
   if (e != cudaSuccess) return e;
   LaunchScope scope(MOE_K_OTHER, st);
   void* params[] = {&a};
