@@ -103,7 +103,7 @@ struct FewShared {
   float sgate[kFewMaxT];                    // zero behind the last token
   float pair_w[kFewPairs];
   int16_t act_e[kFewMaxT * kMaxK + 1];      // entry 0: the shared expert
-  int16_t act_pair[kFewMaxT * kMaxK + 1];   // first pair of the expert
+  int16_t act_pair[kFewMaxT * kMaxK + 2];   // first pair of the expert; behind the last one: pairs
   uint8_t act_mask[kFewMaxT * kMaxK + 1];
   int n_act;
   int aborted;
@@ -434,7 +434,10 @@ __device__ void build_active(const FewArgs& a, FewShared& S) {
     ++at;
     pair += __popc(m[i]);
   }
-  if (tid == 0) S.n_act = 1 + (total >> 16);
+  if (tid == 0) {
+    S.n_act = 1 + (total >> 16);
+    S.act_pair[1 + (total >> 16)] = (int16_t)(a.T + (total & 0xffff));
+  }
   asm volatile("fence.proxy.async;" ::: "memory");  // the logits' place becomes the ring again
   ptx::bar_arrive(kBarRouted, kFewBlock);
   sync_consumers();
@@ -671,21 +674,8 @@ __device__ __forceinline__ void gate_up_tiles(const FewArgs& a, FewShared& S, ui
 // CTA b owns the output rows [b H / grid, (b + 1) H / grid), a.rows (at most 32) in a pass.
 __device__ __forceinline__ int row_begin(const FewArgs& a, int b) { return (int)((int64_t)b * a.H / gridDim.x); }
 
-// Small experts come several to a stage: the active ones [s, s + n), n at most a.group, with `tokens`
-// (at most the units of h there are) between them.
-struct Group {
-  int n, tokens;
-};
-__device__ __forceinline__ Group group_at(const FewArgs& a, const FewShared& S, int s) {
-  Group g{1, __popc(S.act_mask[s])};
-  while (g.n < a.group && s + g.n < S.n_act) {
-    const int t = __popc(S.act_mask[s + g.n]);
-    if (g.tokens + t > a.units) break;
-    g.tokens += t;
-    ++g.n;
-  }
-  return g;
-}
+// Small experts come a.group to a stage, in order; the last stage may hold fewer.
+__device__ __forceinline__ int group_size(const FewArgs& a, const FewShared& S, int s) { return min(a.group, S.n_act - s); }
 
 template <int FMT>
 __device__ void feed_down(Feeder& f, const FewMaps& m) {
@@ -702,22 +692,21 @@ __device__ void feed_down(Feeder& f, const FewMaps& m) {
       tma_4d(dst, &m.dn_s, bar, 0, r0, c * a.dn_s.cb, 0);
       f.end();
     }
-    for (int s = 1; s < f.S.n_act;) {
-      const Group g = group_at(a, f.S, s);
+    for (int s = 1; s < f.S.n_act; s += a.group) {
+      const int n = group_size(a, f.S, s);
       for (int c = 0; c < a.dn.n; ++c) {
         uint8_t* dst = f.begin();
         if (!f.ok) return;
         uint64_t* bar = &f.S.full[f.cur.s];
         f.tag();
-        ptx::mbar_arrive_expect_tx(bar, g.n * (routed + scales));
-        for (int j = 0; j < g.n; ++j, dst += a.slot) {
+        ptx::mbar_arrive_expect_tx(bar, n * (routed + scales));
+        for (int j = 0; j < n; ++j, dst += a.slot) {
           const int e = f.S.act_e[s + j];
           tma_4d(dst, &m.dn, bar, 0, r0, c * a.dn.cb, e);
           if (FMT >= 0) tma_3d(dst + round128(routed), &m.dn_sc, bar, a.dn.scale_at(c, a.shift) & ~15, r0, e);
         }
         f.end();
       }
-      s += g.n;
     }
   }
 }
@@ -738,33 +727,33 @@ __device__ void feed_h(Feeder& f, uint8_t* units) {
     --flight;
   };
   for (int r0 = row_begin(a, blockIdx.x); r0 < n1; r0 += a.rows)
-    for (int s = 0; s < S.n_act;) {
+    for (int s = 0, next; s < S.n_act; s = next) {
       const FewChunks& ch = s ? a.dn : a.dn_s;
-      const Group g = s ? group_at(a, S, s) : Group{1, a.T};
+      next = s ? s + group_size(a, S, s) : 1;
+      const int first = s ? S.act_pair[s] : 0, tokens = s ? S.act_pair[next] - first : a.T;
       const int block = FMT >= 0 && s ? 768 : 192, total = 6 * (s ? a.I : a.Is);
       // the group's pairs follow one another
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(a.h) + (s ? (size_t)S.act_pair[s] : 0) * a.ldh * 6;
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(a.h) + (size_t)first * a.ldh * 6;
       for (int c = 0; c < ch.n; ++c) {
         f.begin();
         if (f.ok && flight == a.stages) pop();  // it was in this place
-        while (f.ok && in_use + g.tokens > a.units) {
+        while (f.ok && in_use + tokens > a.units) {
           f.ok = wait_phase(&S.empty[done.s], done.parity, S, a.status);
           pop();
         }
         if (!f.ok) return;
         const int from = c * ch.cb * block, n = min(ch.cb * block, total - from);
         uint64_t* bar = &f.S.full[f.cur.s];
-        ptx::mbar_arrive_expect_tx(bar, g.tokens * n);
-        for (int q = 0; q < g.tokens; ++q) {
+        ptx::mbar_arrive_expect_tx(bar, tokens * n);
+        for (int q = 0; q < tokens; ++q) {
           bulk_load(units + (size_t)at * a.unit, src + (size_t)q * a.ldh * 6 + from, n, bar);
           if (++at == a.units) at = 0;
         }
-        S.stage_units[f.cur.s] = (uint8_t)g.tokens;
-        in_use += g.tokens;
+        S.stage_units[f.cur.s] = (uint8_t)tokens;
+        in_use += tokens;
         ++flight;
         f.end();
       }
-      s += g.n;
     }
 }
 
@@ -902,54 +891,51 @@ __device__ __forceinline__ void down_stage(const FewArgs& a, FewShared& S, const
   }
 }
 
-// One pass of NI row tiles. The teams take the stages in turn; a stage of one expert is shared by the
-// team, of a stage of several each warp takes one.
+// One pass of NI row tiles. The teams take the stages in turn (`turn`: the team of the pass's first one,
+// `unit`: its first unit of h), and the warps of a team share each of a stage's experts.
 template <int FMT, int NI>
 __device__ __forceinline__ void down_pass(const FewArgs& a, FewShared& S, uint32_t ring, Place& at, int& turn,
                                           uint32_t units, int& unit, int nr, int warp, int lane) {
   const int team = warp / kFewTeam, wt = warp & (kFewTeam - 1);
   for (int i = lane; i < kFewRows * kFewMaxT; i += 32) (&S.out[warp][0][0])[i] = 0.f;
   __syncwarp();
-  auto skip = [&](int tokens) {
-    turn = turn + 1 == kFewTeams ? 0 : turn + 1;
-    unit += tokens;
-    if (unit >= a.units) unit -= a.units;
-    at.skip(1, a.stages);
-  };
+  const int share = kFewTeam / a.group, mine = wt / share;  // warps of an expert; this warp's expert of a group
+  const int groups = (S.n_act - 1 + a.group - 1) / a.group, end = a.dn_s.n + groups * a.dn.n;
+  const int first = team >= turn ? team - turn : team - turn + kFewTeams;
+  const int routed = unit + a.dn_s.n * a.T, pairs = S.act_pair[S.n_act] - a.T;
+  auto wrap = [&](int u) { return u < a.units ? u : u % a.units; };
   auto release = [&] {
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(&S.empty[at.cur.s]);
   };
-  for (int c = 0; c < a.dn_s.n; ++c) {
-    if (turn == team) {
-      wait_stage(at, S, a.status);
-      down_stage<-1, NI>(a, S, a.dn_s, ring + at.cur.s * a.stage_bytes, units, unit, (1u << a.T) - 1u, c, true, nr,
-                         wt, kFewTeam, warp, lane);
-      release();
-    }
-    skip(a.T);
+  int j = first;
+  at.skip(first, a.stages);
+  for (; j < a.dn_s.n; j += kFewTeams, at.skip(kFewTeams, a.stages)) {
+    wait_stage(at, S, a.status);
+    down_stage<-1, NI>(a, S, a.dn_s, ring + at.cur.s * a.stage_bytes, units, wrap(unit + j * a.T), (1u << a.T) - 1u, j,
+                       true, nr, wt, kFewTeam, warp, lane);
+    release();
   }
-  for (int s = 1; s < S.n_act;) {
-    const Group g = group_at(a, S, s);
-    for (int c = 0; c < a.dn.n; ++c) {
-      if (turn == team) {
-        const uint32_t st = ring + at.cur.s * a.stage_bytes;
-        wait_stage(at, S, a.status);
-        if (g.n == 1) {
-          down_stage<FMT, NI>(a, S, a.dn, st, units, unit, S.act_mask[s], c, false, nr, wt, kFewTeam, warp, lane);
-        } else if (wt < g.n) {
-          int u = unit;
-          for (int j = 0; j < wt; ++j) u += __popc(S.act_mask[s + j]);
-          if (u >= a.units) u -= a.units;
-          down_stage<FMT, NI>(a, S, a.dn, st + wt * a.slot, units, u, S.act_mask[s + wt], c, false, nr, 0, 1, warp,
-                              lane);
-        }
-        release();
-      }
-      skip(g.tokens);
-    }
-    s += g.n;
+  int s = 1, c = j - a.dn_s.n;  // the group's first expert, chunk
+  for (; j < end; j += kFewTeams, c += kFewTeams, at.skip(kFewTeams, a.stages)) {
+    for (; c >= a.dn.n; c -= a.dn.n) s += a.group;
+    // chunk by chunk, a group's units follow one another as its pairs do
+    const int e = s + mine, base = S.act_pair[s], n = S.act_pair[min(s + a.group, S.n_act)] - base;
+    const int mask = e < S.n_act ? S.act_mask[e] : 0;
+    const int u = wrap(routed + (base - a.T) * a.dn.n + c * n + (mask ? S.act_pair[e] - base : 0));
+    wait_stage(at, S, a.status);
+    down_stage<FMT, NI>(a, S, a.dn, ring + at.cur.s * a.stage_bytes + mine * a.slot, units, u, mask, c, false, nr,
+                        wt & (share - 1), share, warp, lane);
+    release();
   }
+  at.i -= j - end;  // back to the first stage of the next pass
+  at.cur.s -= j - end;
+  if (at.cur.s < 0) {
+    at.cur.s += a.stages;
+    at.cur.parity ^= 1u;
+  }
+  turn = (turn + end) % kFewTeams;
+  unit = wrap(routed + pairs * a.dn.n);
 }
 
 template <int FMT>
@@ -1314,7 +1300,9 @@ cudaError_t launch_few_layer(const moe_shape& s, const Layout& L, char* ws, cons
   a.h_bytes = ((int)kFewSmem - (int)kFewSharedBytes - a.stages * a.stage_bytes) / 128 * 128;
   a.units = std::min(a.h_bytes / a.unit, 64);
   a.slot = (a.rows * 64 * a.dn.cb + 127) / 128 * 128 + (a.rows * a.dn.sc + 127) / 128 * 128;
-  a.group = a.dn.n == 1 ? std::min(a.stage_bytes / a.slot, kFewTeam) : 1;
+  // experts of a stage: 1, 2 or 4, so that each has as many of the team's warps
+  const int fit = std::min(a.stage_bytes / a.slot, a.units / s.T);
+  a.group = a.dn.n > 1 || fit < 2 ? 1 : fit < kFewTeam ? 2 : kFewTeam;
 
   FewMaps m;
   bool ok = few_weight_map(&m.gu_s, w.ws_gate_up, s.Is, a.gu_s, 2 * (uint64_t)s.H, 2, 1, 8) &&
