@@ -543,6 +543,14 @@ __device__ __forceinline__ void tile_bf16(const FewArgs& a, FewShared& S, const 
   }
 }
 
+// A half block, the last one of a row: parts 2 and 3 are multiplied by zero. The scale of a group
+// that lies behind the row is not read either (a group of 128 has its first half in the row).
+template <int FMT>
+__device__ __forceinline__ void w4_half(uint4 (&x)[4], uint2& s0, uint2& s1) {
+  x[2] = x[3] = make_uint4(0u, 0u, 0u, 0u);
+  if (FMT < 2) s0.y = s1.y = 0u;
+}
+
 // The same for 4-bit weights. Their operands come out of arithmetic and can go to any register, so
 // the MMA's A is the 8 gate rows and the 8 up rows, and its columns are the tokens. Chunks c, c + step, ...
 // acc[0], [1]: gate row g, tokens 2 t and 2 t + 1; acc[2], [3]: the up row.
@@ -552,7 +560,7 @@ __device__ __forceinline__ void tile_w4(const FewArgs& a, FewShared& S, const Fe
                                         float (&acc)[4]) {
   const int g = lane >> 2, t4 = lane & 3, wt = warp & (kFewTeam - 1), tok = g < a.T;
   const uint32_t xg = xs + g * xpitch + 16 * t4;
-  uint4 x = make_uint4(0u, 0u, 0u, 0u);  // stays zero in the lanes of no token
+  uint4 x[4] = {};  // stays zero in the lanes of no token
   for (at.skip(c, a.stages); c < ch.n; c += step, at.skip(step, a.stages)) {
     const uint32_t st = ring + at.cur.s * a.stage_bytes;
     const int b0 = c * ch.cb, nb = min(ch.cb, ch.blocks - b0);
@@ -561,19 +569,20 @@ __device__ __forceinline__ void tile_w4(const FewArgs& a, FewShared& S, const Fe
     const uint32_t up_at = 512 * ch.cb, sp = st + 1024 * ch.cb + g * ch.sc + (ch.scale_at(c, FMT) & 15);
     for (int b = wt; b < nb; b += kFewTeam, wp += 512 * kFewTeam, xp += 256 * kFewTeam) {
       const uint4 wg = lds_v4(wp), wu = lds_v4(wp + up_at);
-      const uint2 sg = w4_block_scales<FMT>(sp, b), su = w4_block_scales<FMT>(sp + 8 * ch.sc, b);
-      const int parts = min(4, a.H / 32 - 4 * (b0 + b));
+      uint2 sg = w4_block_scales<FMT>(sp, b), su = w4_block_scales<FMT>(sp + 8 * ch.sc, b);
+      const bool half = a.H / 32 - 4 * (b0 + b) == 2;  // H is a multiple of 64: four parts or two
+#pragma unroll
+      for (int j = 0; j < 4; ++j) lds_v4_if(x[j], xp + 64 * j, tok && (j < 2 || !half));
+      if (half) w4_half<FMT>(x, sg, su);
       float d[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (j >= 2 && j >= parts) break;  // H is a multiple of 64: two parts or four
         const uint4 pg = w4_pairs<false>(word(wg, j)), pu = w4_pairs<false>(word(wu, j));
-        lds_v4_if(x, xp + 64 * j, tok);
         // the parts of a group share a chain and a scale
-        if (j % (1 << FMT) == 0) mma16816_first<false>(d, pg.x, pu.x, pg.y, pu.y, x.x, x.y);
-        else mma16816<false>(d, pg.x, pu.x, pg.y, pu.y, x.x, x.y);
-        mma16816<false>(d, pg.z, pu.z, pg.w, pu.w, x.z, x.w);
-        if ((j + 1) % (1 << FMT) == 0 || (j == 1 && parts == 2)) {
+        if (j % (1 << FMT) == 0) mma16816_first<false>(d, pg.x, pu.x, pg.y, pu.y, x[j].x, x[j].y);
+        else mma16816<false>(d, pg.x, pu.x, pg.y, pu.y, x[j].x, x[j].y);
+        mma16816<false>(d, pg.z, pu.z, pg.w, pu.w, x[j].z, x[j].w);
+        if ((j + 1) % (1 << FMT) == 0) {
           const float fg = w4_scale(sg, j), fu = w4_scale(su, j);
           acc[0] = fmaf(d[0], fg, acc[0]);
           acc[1] = fmaf(d[1], fg, acc[1]);
@@ -813,7 +822,7 @@ __device__ __forceinline__ void down_bf16(const FewArgs& a, FewShared& S, uint32
 }
 
 // 4-bit weights: the MMA's A is 16 rows, its columns 0-2 and 4-6 are one or two tokens' pieces.
-template <int FMT, int NP>
+template <int FMT, int NI>
 __device__ __forceinline__ void down_w4(const FewArgs& a, FewShared& S, const FewChunks& ch, uint32_t st,
                                         uint32_t units, int unit, uint32_t mask, int c, int nb, int nr, int wt,
                                         int step, int warp, int lane) {
@@ -825,38 +834,48 @@ __device__ __forceinline__ void down_w4(const FewArgs& a, FewShared& S, const Fe
   uint32_t hu = units + u * a.unit + 64 * (g & 3) + 16 * t4 + wt * 768;
   uint32_t wp = st + 64 * wt * a.rows + 16 * t4;
   const uint32_t sp = st + round128(a.rows * 64 * ch.cb) + (ch.scale_at(c, FMT) & 15);
-  uint32_t row[2 * NP];  // rows behind the pass read its last one
+  constexpr int NP = (NI + 1) / 2;  // an odd last tile is both halves of its MMA, the second for nothing
+  uint32_t row[NI];                 // rows behind the pass read its last one
 #pragma unroll
-  for (int i = 0; i < 2 * NP; ++i) row[i] = min(8 * i + g, nr - 1);
-  uint4 x = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = 0; i < NI; ++i) row[i] = min(8 * i + g, nr - 1);
+  uint4 x[4] = {};
   float sum[NP][4] = {};
   for (int b = wt; b < nb; b += step, wp += 64 * step * a.rows, hu += 768 * step) {
-    uint4 w[2 * NP];
-    uint2 sc[2 * NP];
+    const bool half = K / 32 - 4 * (b0 + b) == 2;  // K is a multiple of 64: four parts or two
+    uint4 w[NI];
+    uint2 sc[NI];
 #pragma unroll
-    for (int i = 0; i < 2 * NP; ++i) {
+    for (int i = 0; i < NI; ++i) {
       w[i] = lds_v4(wp + 64 * row[i]);
       sc[i] = w4_block_scales<FMT>(sp + row[i] * ch.sc, b);
     }
-    const int parts = min(4, K / 32 - 4 * (b0 + b));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) lds_v4_if(x[j], hu + 192 * j, piece && (j < 2 || !half));
+    if (half) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) w4_half<FMT>(x, sc[i], sc[i]);
+    }
     float d[NP][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (j >= 2 && j >= parts) break;  // K is a multiple of 64: two parts or four
-      lds_v4_if(x, hu + 192 * j, piece);
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
-        const uint4 v = w4_pairs<false>(word(w[2 * p], j)), v8 = w4_pairs<false>(word(w[2 * p + 1], j));
+        const bool both = 2 * p + 1 < NI;
+        const int p8 = both ? 2 * p + 1 : 2 * p;
+        const uint4 v = w4_pairs<false>(word(w[2 * p], j)), v8 = both ? w4_pairs<false>(word(w[p8], j)) : v;
         // the parts of a group share a chain and a scale
-        if (j % (1 << FMT) == 0) mma16816_first<false>(d[p], v.x, v8.x, v.y, v8.y, x.x, x.y);
-        else mma16816<false>(d[p], v.x, v8.x, v.y, v8.y, x.x, x.y);
-        mma16816<false>(d[p], v.z, v8.z, v.w, v8.w, x.z, x.w);
-        if ((j + 1) % (1 << FMT) == 0 || (j == 1 && parts == 2)) {
-          const float f = w4_scale(sc[2 * p], j), f8 = w4_scale(sc[2 * p + 1], j);
+        if (j % (1 << FMT) == 0) mma16816_first<false>(d[p], v.x, v8.x, v.y, v8.y, x[j].x, x[j].y);
+        else mma16816<false>(d[p], v.x, v8.x, v.y, v8.y, x[j].x, x[j].y);
+        mma16816<false>(d[p], v.z, v8.z, v.w, v8.w, x[j].z, x[j].w);
+        if ((j + 1) % (1 << FMT) == 0) {
+          const float f = w4_scale(sc[2 * p], j);
           sum[p][0] = fmaf(d[p][0], f, sum[p][0]);
           sum[p][1] = fmaf(d[p][1], f, sum[p][1]);
-          sum[p][2] = fmaf(d[p][2], f8, sum[p][2]);
-          sum[p][3] = fmaf(d[p][3], f8, sum[p][3]);
+          if (both) {
+            const float f8 = w4_scale(sc[p8], j);
+            sum[p][2] = fmaf(d[p][2], f8, sum[p][2]);
+            sum[p][3] = fmaf(d[p][3], f8, sum[p][3]);
+          }
         }
       }
     }
@@ -864,7 +883,7 @@ __device__ __forceinline__ void down_w4(const FewArgs& a, FewShared& S, const Fe
   // lanes t = 0, 1: the first token's pieces 0 and 1, and 2; t = 2, 3: the second's
   const int token = t4 < 2 ? __ffs(mask) - 1 : __ffs(mask & (mask - 1)) - 1;
 #pragma unroll
-  for (int i = 0; i < 2 * NP; ++i) {
+  for (int i = 0; i < NI; ++i) {
     float v = sum[i / 2][2 * (i % 2)] + (t4 & 1 ? 0.f : sum[i / 2][2 * (i % 2) + 1]);
     v += __shfl_xor_sync(0xffffffffu, v, 1);
     if (t4 == 0 || (t4 == 2 && two)) S.out[warp][8 * i + g][token] += v;
@@ -879,7 +898,7 @@ __device__ __forceinline__ void down_stage(const FewArgs& a, FewShared& S, const
   const int nb = min(ch.cb, ch.blocks - c * ch.cb);
   for (uint32_t left = mask; left;) {  // two tokens at a time
     if constexpr (FMT >= 0)
-      down_w4<FMT, (NI + 1) / 2>(a, S, ch, st, units, unit, left, c, nb, nr, wt, step, warp, lane);
+      down_w4<FMT, NI>(a, S, ch, st, units, unit, left, c, nb, nr, wt, step, warp, lane);
     else if (left & (left - 1))
       down_bf16<NI, 2>(a, S, st, units, unit, left, nb, nr, wt, step, gated, warp, lane);
     else
