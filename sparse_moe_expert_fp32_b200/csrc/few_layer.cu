@@ -527,8 +527,8 @@ __device__ __forceinline__ void tile_bf16(const FewArgs& a, FewShared& S, const 
       for (int q = 0; q < NQ; ++q) {
         lds_v4_if(x[q], xp + 4 * q * xpitch, tok[q]);
         const uint2 y = make_uint2(low ? x[q].x : x[q].y, low ? x[q].z : x[q].w);
-        mma_rows<false>(dg[q], wg, y);
-        mma_rows<false>(du[q], wu, y);
+        mma_rows(dg[q], wg, y);
+        mma_rows(du[q], wu, y);
       }
     }
 #pragma unroll
@@ -802,7 +802,7 @@ __device__ __forceinline__ void down_bf16(const FewArgs& a, FewShared& S, uint32
     for (int i = 0; i < NI; ++i) {
       const uint4 w = lds_v4(wp + (i < NI - 1 ? row + 512 * i : last));
 #pragma unroll
-      for (int n = 0; n < N; ++n) mma_rows<false>(sum[n][i], w, y[n]);
+      for (int n = 0; n < N; ++n) mma_rows(sum[n][i], w, y[n]);
     }
   }
 #pragma unroll

@@ -64,17 +64,8 @@ __device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint3
 // and 2 of a column's 16 bytes) and columns 4-7 those of the second (registers 1 and 3): four columns
 // of x, d[0], d[1] of lanes t < 2 and d[2], d[3] of lanes t >= 2 hold the two halves of their sums,
 // and the rest of D means nothing. See fold().
-template <bool FIRST>
 __device__ __forceinline__ void mma_rows(float (&d)[4], const uint4& w, const uint2& x) {
-  if constexpr (FIRST) mma16816_first<false>(d, w.x, w.y, w.z, w.w, x.x, x.y);
-  else mma16816<false>(d, w.x, w.y, w.z, w.w, x.x, x.y);
-}
-// 8 weight rows by 32 elements as B, 16 rows of x as A: two quads {x[g], x[g + 8]} x {registers 0, 1}
-// and x {registers 2, 3}. D: d[0], d[1]: row g of x, weight rows 2 t and 2 t + 1; d[2], d[3]: row g + 8.
-template <bool F16>
-__device__ __forceinline__ void mma_cols(float (&d)[4], const uint4& x0, const uint4& x1, const uint4& w) {
-  mma16816_first<F16>(d, x0.x, x0.y, x0.z, x0.w, w.x, w.y);
-  mma16816<F16>(d, x1.x, x1.y, x1.z, x1.w, w.z, w.w);
+  mma16816<false>(d, w.x, w.y, w.z, w.w, x.x, x.y);
 }
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
@@ -95,12 +86,6 @@ __device__ __forceinline__ void lds_v4_if(uint4& v, uint32_t at, int p) {
                : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
                : "r"(at), "r"(p));
 }
-__device__ __forceinline__ void lds_v2_if(uint2& v, uint32_t at, int p) {
-  asm volatile("{\n .reg .pred q;\n setp.ne.s32 q, %3, 0;\n @q ld.shared.v2.u32 {%0,%1}, [%2];\n}\n"
-               : "+r"(v.x), "+r"(v.y)
-               : "r"(at), "r"(p));
-}
-
 __device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
   uint32_t r;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(mask), "r"(bits));

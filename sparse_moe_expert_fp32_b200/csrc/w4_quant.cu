@@ -10,9 +10,9 @@
 //
 // The quotient without a division: with 8-bit significands w / scale is either exactly half
 // way between two integers or at least 2^-10 away from it (for |w / scale| >= 1/4 its
-// distance is a multiple of 1/2 over twice an 8-bit integer). fma(w, 1 / scale, 3072) is it
+// distance is a multiple of 1/2 over twice an 8-bit integer). fma(w, 1 / scale, 2^11 + 2^10) is it
 // to a multiple of 2^-12, off by less than that, so an exact tie is exact again and nothing
-// else has crossed one; adding 2^23 + 2^22 + 8 - 3072 rounds it to an integer, ties to even, and
+// else has crossed one; adding 2^23 + 2^22 + 8 - 2^11 - 2^10 rounds it to an integer, ties to even, and
 // leaves code in the low bits. Scales so small that the reciprocal leaves fp32's range divide
 // instead. amax / 7 has no such ties (7 divides no odd multiple of a half step), so a
 // multiplication by 1/7 rounds to the same bf16.
@@ -26,7 +26,7 @@ constexpr int kQuantThreads = 256;
 
 // eight bf16 of a row at element e (zeros behind the row's end)
 template <bool VEC>
-__device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t e, int64_t K) {
+__device__ __forceinline__ uint4 load8(const uint16_t* row, uint32_t e, uint32_t K) {
   uint4 v = make_uint4(0u, 0u, 0u, 0u);
   if constexpr (VEC) {
     if (e < K) v = ld_stream_v4(row + e);
@@ -40,10 +40,12 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t e, int64_t K
 }
 
 // Blocks i, i + stride, ... of a matrix with `per_row` blocks a row, without a division a step.
+// The numbers are 32-bit (at most 2^31 rows of 2^20 elements), so that an address is one wide
+// multiplication.
 struct BlockWalk {
-  int64_t row, b, per_row, row_step, b_step;
-  __device__ BlockWalk(int64_t i, int64_t stride, int64_t per_row)
-      : row(i / per_row), b(i % per_row), per_row(per_row), row_step(stride / per_row), b_step(stride % per_row) {}
+  uint32_t row, b, per_row, row_step, b_step;
+  __device__ BlockWalk(uint32_t first, uint32_t stride, uint32_t per_row)
+      : row(first / per_row), b(first % per_row), per_row(per_row), row_step(stride / per_row), b_step(stride % per_row) {}
   __device__ void next() {
     row += row_step;
     b += b_step;
@@ -78,7 +80,7 @@ __device__ __forceinline__ uint32_t codes8(const uint4& v, float s) {
   uint32_t c[8];
   if (s >= 0x1p-100f) {
     const float inv = __frcp_rn(s);
-    const uint64_t inv2 = pack2(inv, inv), snap = pack2(3072.f, 3072.f), whole = pack2(12579848.f, 12579848.f);
+    const uint64_t inv2 = pack2(inv, inv), snap = pack2(0x1.8p11f, 0x1.8p11f), whole = pack2(12579848.f, 12579848.f);
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
       const uint64_t r = add2(fma2(pack2(f[i], f[i + 1]), inv2, snap), whole);
@@ -99,25 +101,24 @@ __device__ __forceinline__ uint32_t codes8(const uint4& v, float s) {
 
 template <bool VEC, int SHIFT>
 __global__ void __launch_bounds__(kQuantThreads)
-quantize_w4_kernel(const uint16_t* __restrict__ w, int64_t rows, int64_t K, uint8_t* __restrict__ q,
+quantize_w4_kernel(const uint16_t* __restrict__ w, uint32_t rows, int64_t K, uint8_t* __restrict__ q,
                    uint16_t* __restrict__ scales) {
   const int lane = threadIdx.x & 15, j = lane >> 2, t = lane & 3;
-  const int64_t blocks = w4_blocks(K);
-  const int64_t ns = w4_row_scales(K, 32 << SHIFT);
-  const int64_t vblocks = (ns << SHIFT) >> 2;  // blocks with the scale padding's share, >= blocks
-  const int64_t stride = (int64_t)gridDim.x * (kQuantThreads / 16);
+  const uint32_t blocks = (uint32_t)w4_blocks(K), ns = (uint32_t)w4_row_scales(K, 32 << SHIFT), k = (uint32_t)K;
+  const uint32_t vblocks = (ns << SHIFT) >> 2;  // blocks with the scale padding's share, >= blocks
+  const uint32_t stride = gridDim.x * (kQuantThreads / 16);
   constexpr int lanes = 4 << SHIFT;  // lanes of a group
-  BlockWalk at((int64_t)blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4), stride, vblocks);
+  BlockWalk at(blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4), stride, vblocks);
   // both halves of a warp stay in the loop as long as one has a block (the shuffles)
   while (__any_sync(0xffffffffu, at.row < rows)) {
     uint4 v[kQuantBatch];
-    int64_t row[kQuantBatch], b[kQuantBatch];
+    uint32_t row[kQuantBatch], b[kQuantBatch];
 #pragma unroll
     for (int u = 0; u < kQuantBatch; ++u) {
       row[u] = at.row;
       b[u] = at.b;
       v[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (at.row < rows && at.b < blocks) v[u] = load8<VEC>(w + at.row * K, at.b * kW4Block + 32 * j + 8 * t, K);
+      if (at.row < rows && at.b < blocks) v[u] = load8<VEC>(w + (uint64_t)at.row * k, at.b * kW4Block + 32 * j + 8 * t, k);
       at.next();
     }
 #pragma unroll
@@ -133,9 +134,9 @@ quantize_w4_kernel(const uint16_t* __restrict__ w, int64_t rows, int64_t K, uint
           m >= 0x7f80u ? (uint16_t)0x7fc0u : f32_to_bf16_rn(__uint_as_float(m << 16) * (1.f / 7.f));
       if (row[u] >= rows) continue;
       // a group has one writer: its first lane
-      if ((lane & (lanes - 1)) == 0) scales[row[u] * ns + ((b[u] * 4 + j) >> SHIFT)] = sb;
+      if ((lane & (lanes - 1)) == 0) scales[(uint64_t)row[u] * ns + ((b[u] * 4 + j) >> SHIFT)] = sb;
       if (b[u] < blocks)
-        *reinterpret_cast<uint32_t*>(q + (row[u] * blocks + b[u]) * kW4BlockBytes + 16 * t + 4 * j) =
+        *reinterpret_cast<uint32_t*>(q + ((uint64_t)row[u] * blocks + b[u]) * kW4BlockBytes + 16 * t + 4 * j) =
             codes8(v[u], __uint_as_float((uint32_t)sb << 16));
     }
   }
@@ -145,32 +146,31 @@ quantize_w4_kernel(const uint16_t* __restrict__ w, int64_t rows, int64_t K, uint
 template <bool VEC, bool BF16, int SHIFT>
 __global__ void __launch_bounds__(kQuantThreads)
 dequantize_w4_kernel(const uint8_t* __restrict__ q, const uint16_t* __restrict__ scales,
-                     int64_t rows, int64_t K, void* __restrict__ out) {
+                     uint32_t rows, int64_t K, void* __restrict__ out) {
   const int lane = threadIdx.x & 15, j = lane >> 2, t = lane & 3;
-  const int64_t blocks = w4_blocks(K);
-  const int64_t ns = w4_row_scales(K, 32 << SHIFT);
-  const int64_t stride = (int64_t)gridDim.x * (kQuantThreads / 16);
-  BlockWalk at((int64_t)blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4), stride, blocks);
+  const uint32_t blocks = (uint32_t)w4_blocks(K), ns = (uint32_t)w4_row_scales(K, 32 << SHIFT), k = (uint32_t)K;
+  const uint32_t stride = gridDim.x * (kQuantThreads / 16);
+  BlockWalk at(blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4), stride, blocks);
   while (at.row < rows) {
     uint32_t word[kQuantBatch], scale[kQuantBatch];
-    int64_t row[kQuantBatch], first[kQuantBatch];
+    uint32_t row[kQuantBatch], first[kQuantBatch];
 #pragma unroll
     for (int u = 0; u < kQuantBatch; ++u) {
       row[u] = at.row;
       first[u] = at.b * kW4Block + 32 * j + 8 * t;
       word[u] = scale[u] = 0u;
-      if (at.row < rows && first[u] < K) {
-        word[u] = __ldg(reinterpret_cast<const uint32_t*>(q + (at.row * blocks + at.b) * kW4BlockBytes + 16 * t + 4 * j));
-        scale[u] = __ldg(scales + at.row * ns + ((at.b * 4 + j) >> SHIFT));
+      if (at.row < rows && first[u] < k) {
+        word[u] = __ldg(reinterpret_cast<const uint32_t*>(q + ((uint64_t)at.row * blocks + at.b) * kW4BlockBytes + 16 * t + 4 * j));
+        scale[u] = __ldg(scales + (uint64_t)at.row * ns + ((at.b * 4 + j) >> SHIFT));
       }
       at.next();
     }
 #pragma unroll
     for (int u = 0; u < kQuantBatch; ++u) {
-      if (row[u] >= rows || first[u] >= K) continue;
+      if (row[u] >= rows || first[u] >= k) continue;
       const uint4 c = w4_pairs<false>(word[u]);  // c - 8 as bf16, exactly
-      const int64_t e = row[u] * K + first[u];
-      const int n = (int)min((int64_t)8, K - first[u]);
+      const uint64_t e = (uint64_t)row[u] * k + first[u];
+      const int n = (int)min(8u, k - first[u]);
       if constexpr (BF16) {
         uint16_t* o = static_cast<uint16_t*>(out) + e;
         const uint32_t s2 = scale[u] * 0x10001u;
@@ -218,7 +218,7 @@ cudaError_t launch_quantize_w4(const uint16_t* w, int64_t rows, int64_t K, int s
   LaunchScope scope(MOE_K_OTHER, st);
   const int grid = quant_blocks(items, sms);
 #define MOE_QUANT(VEC, SH) \
-  quantize_w4_kernel<VEC, SH><<<grid, kQuantThreads, 0, st>>>(w, rows, K, q, scales)
+  quantize_w4_kernel<VEC, SH><<<grid, kQuantThreads, 0, st>>>(w, (uint32_t)rows, K, q, scales)
   if (K % 8 == 0) {
     if (shift == 0) MOE_QUANT(true, 0);
     else if (shift == 1) MOE_QUANT(true, 1);
@@ -236,9 +236,9 @@ namespace {
 template <bool VEC, bool BF16>
 void dequantize(const uint8_t* q, const uint16_t* scales, int64_t rows, int64_t K, int shift, void* out, int grid,
                 cudaStream_t st) {
-  if (shift == 0) dequantize_w4_kernel<VEC, BF16, 0><<<grid, kQuantThreads, 0, st>>>(q, scales, rows, K, out);
-  else if (shift == 1) dequantize_w4_kernel<VEC, BF16, 1><<<grid, kQuantThreads, 0, st>>>(q, scales, rows, K, out);
-  else dequantize_w4_kernel<VEC, BF16, 2><<<grid, kQuantThreads, 0, st>>>(q, scales, rows, K, out);
+  if (shift == 0) dequantize_w4_kernel<VEC, BF16, 0><<<grid, kQuantThreads, 0, st>>>(q, scales, (uint32_t)rows, K, out);
+  else if (shift == 1) dequantize_w4_kernel<VEC, BF16, 1><<<grid, kQuantThreads, 0, st>>>(q, scales, (uint32_t)rows, K, out);
+  else dequantize_w4_kernel<VEC, BF16, 2><<<grid, kQuantThreads, 0, st>>>(q, scales, (uint32_t)rows, K, out);
 }
 }  // namespace
 
