@@ -24,17 +24,36 @@ namespace {
 
 constexpr int kQuantThreads = 256;
 
-// eight bf16 of a row at element e (zeros behind the row's end)
+// Eight bf16 of row r at element e, zeros behind the row's end. Where rows do not start on 16 bytes
+// (VEC false) they come as the five aligned words that hold them, except at the matrix's two ends.
 template <bool VEC>
-__device__ __forceinline__ uint4 load8(const uint16_t* row, uint32_t e, uint32_t K) {
+__device__ __forceinline__ uint4 load8(const uint16_t* w, uint32_t r, uint32_t e, uint32_t K, uint64_t total) {
   uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (e >= K) return v;
+  const uint64_t at = (uint64_t)r * K + e;
+  const uint16_t* p = w + at;
   if constexpr (VEC) {
-    if (e < K) v = ld_stream_v4(row + e);
+    v = ld_stream_v4(p);
   } else {
     uint32_t* u = &v.x;
+    const int n = (int)min(8u, K - e);
+    if (at > 0 && at + 9 <= total) {
+      const bool odd = (reinterpret_cast<uintptr_t>(p) & 2u) != 0;
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(p - odd);
+      uint32_t x[5];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (e + i < K) u[i >> 1] |= (uint32_t)__ldg(row + e + i) << (16 * (i & 1));
+      for (int i = 0; i < 4; ++i) x[i] = __ldg(q + i);
+      x[4] = odd ? __ldg(q + 4) : 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        u[i] = odd ? __byte_perm(x[i], x[i + 1], 0x5432) : x[i];
+        if (2 * i + 1 >= n) u[i] = 2 * i < n ? u[i] & 0xffffu : 0u;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) u[i >> 1] |= (uint32_t)__ldg(p + i) << (16 * (i & 1));
+    }
   }
   return v;
 }
@@ -118,7 +137,8 @@ quantize_w4_kernel(const uint16_t* __restrict__ w, uint32_t rows, int64_t K, uin
       row[u] = at.row;
       b[u] = at.b;
       v[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (at.row < rows && at.b < blocks) v[u] = load8<VEC>(w + (uint64_t)at.row * k, at.b * kW4Block + 32 * j + 8 * t, k);
+      if (at.row < rows && at.b < blocks)
+        v[u] = load8<VEC>(w, at.row, at.b * kW4Block + 32 * j + 8 * t, k, (uint64_t)rows * k);
       at.next();
     }
 #pragma unroll
@@ -142,24 +162,54 @@ quantize_w4_kernel(const uint16_t* __restrict__ w, uint32_t rows, int64_t K, uin
   }
 }
 
+// A block of 128 values of a row to a place without alignment: through shared memory, so that the
+// half warp's stores lie side by side. `n`: the values that are in the row.
+__device__ __forceinline__ void store_block(float* buf, const uint4& v, uint16_t* o, int n, int lane, uint32_t mask) {
+  uint32_t* b = reinterpret_cast<uint32_t*>(buf);
+  reinterpret_cast<uint4*>(b)[lane] = v;
+  __syncwarp(mask);
+  const int odd = (int)((reinterpret_cast<uintptr_t>(o) >> 1) & 1u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = lane + 16 * i, e = 2 * k + odd;
+    const uint32_t two = odd ? __byte_perm(b[k], b[min(k + 1, 63)], 0x5432) : b[k];
+    if (e + 1 < n) *reinterpret_cast<uint32_t*>(o + e) = two;
+    else if (e < n) o[e] = (uint16_t)two;
+  }
+  if (odd && lane == 0) o[0] = (uint16_t)b[0];
+  __syncwarp(mask);
+}
+__device__ __forceinline__ void store_block(float* buf, const float (&f)[8], float* o, int n, int lane, uint32_t mask) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) buf[8 * lane + i] = f[i];
+  __syncwarp(mask);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (lane + 16 * i < n) o[lane + 16 * i] = buf[lane + 16 * i];
+  __syncwarp(mask);
+}
+
 // The inverse: (c - 8) s is exact in fp32 (4 by 8 significant bits); bf16 rounds it once.
 template <bool VEC, bool BF16, int SHIFT>
 __global__ void __launch_bounds__(kQuantThreads)
 dequantize_w4_kernel(const uint8_t* __restrict__ q, const uint16_t* __restrict__ scales,
                      uint32_t rows, int64_t K, void* __restrict__ out) {
   const int lane = threadIdx.x & 15, j = lane >> 2, t = lane & 3;
+  __shared__ __align__(16) float lines[VEC ? 1 : kQuantThreads / 16][kW4Block];
+  float* buf = lines[VEC ? 0 : threadIdx.x >> 4];
+  const uint32_t half = 0xffffu << (threadIdx.x & 16);
   const uint32_t blocks = (uint32_t)w4_blocks(K), ns = (uint32_t)w4_row_scales(K, 32 << SHIFT), k = (uint32_t)K;
   const uint32_t stride = gridDim.x * (kQuantThreads / 16);
   BlockWalk at(blockIdx.x * (kQuantThreads / 16) + (threadIdx.x >> 4), stride, blocks);
   while (at.row < rows) {
     uint32_t word[kQuantBatch], scale[kQuantBatch];
-    uint32_t row[kQuantBatch], first[kQuantBatch];
+    uint32_t row[kQuantBatch], b[kQuantBatch];
 #pragma unroll
     for (int u = 0; u < kQuantBatch; ++u) {
       row[u] = at.row;
-      first[u] = at.b * kW4Block + 32 * j + 8 * t;
+      b[u] = at.b;
       word[u] = scale[u] = 0u;
-      if (at.row < rows && first[u] < k) {
+      if (at.row < rows && at.b * kW4Block + 32 * j + 8 * t < k) {
         word[u] = __ldg(reinterpret_cast<const uint32_t*>(q + ((uint64_t)at.row * blocks + at.b) * kW4BlockBytes + 16 * t + 4 * j));
         scale[u] = __ldg(scales + (uint64_t)at.row * ns + ((at.b * 4 + j) >> SHIFT));
       }
@@ -167,36 +217,28 @@ dequantize_w4_kernel(const uint8_t* __restrict__ q, const uint16_t* __restrict__
     }
 #pragma unroll
     for (int u = 0; u < kQuantBatch; ++u) {
-      if (row[u] >= rows || first[u] >= k) continue;
+      if (row[u] >= rows) continue;
       const uint4 c = w4_pairs<false>(word[u]);  // c - 8 as bf16, exactly
-      const uint64_t e = (uint64_t)row[u] * k + first[u];
-      const int n = (int)min(8u, k - first[u]);
+      const uint64_t at = (uint64_t)row[u] * k + b[u] * kW4Block;
+      const int n = (int)min((uint32_t)kW4Block, k - b[u] * kW4Block);
       if constexpr (BF16) {
-        uint16_t* o = static_cast<uint16_t*>(out) + e;
+        uint16_t* o = static_cast<uint16_t*>(out) + at;
         const uint32_t s2 = scale[u] * 0x10001u;
         const uint4 r = make_uint4(mul_bf16x2(c.x, s2), mul_bf16x2(c.y, s2), mul_bf16x2(c.z, s2), mul_bf16x2(c.w, s2));
-        if constexpr (VEC) {
-          *reinterpret_cast<uint4*>(o) = r;
-        } else {
-          const uint32_t p[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (i < n) o[i] = (uint16_t)(p[i / 2] >> (16 * (i & 1)));
-        }
+        if constexpr (!VEC) store_block(buf, r, o, n, lane, half);
+        else if (8 * lane < n) reinterpret_cast<uint4*>(o)[lane] = r;
       } else {
-        float* o = static_cast<float*>(out) + e;
+        float* o = static_cast<float*>(out) + at;
         const float s = bf16lo(scale[u]);
         float f[8];
         unpack8(c, f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] *= s;
-        if constexpr (VEC) {
-          reinterpret_cast<float4*>(o)[0] = make_float4(f[0], f[1], f[2], f[3]);
-          reinterpret_cast<float4*>(o)[1] = make_float4(f[4], f[5], f[6], f[7]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (i < n) o[i] = f[i];
+        if constexpr (!VEC) {
+          store_block(buf, f, o, n, lane, half);
+        } else if (8 * lane < n) {
+          reinterpret_cast<float4*>(o)[2 * lane] = make_float4(f[0], f[1], f[2], f[3]);
+          reinterpret_cast<float4*>(o)[2 * lane + 1] = make_float4(f[4], f[5], f[6], f[7]);
         }
       }
     }
@@ -205,7 +247,7 @@ dequantize_w4_kernel(const uint8_t* __restrict__ q, const uint16_t* __restrict__
 
 int quant_blocks(int64_t items, int sms) {
   const int64_t per = kQuantThreads / 16;
-  const int64_t need = (items + per - 1) / per, most = (int64_t)sms * 8;
+  const int64_t need = (items + per - 1) / per, most = (int64_t)sms * 32;
   return (int)(need < most ? need : most);
 }
 
