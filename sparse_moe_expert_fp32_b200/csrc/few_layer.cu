@@ -627,10 +627,10 @@ __device__ __forceinline__ void gate_up_tiles(const FewArgs& a, FewShared& S, ui
         tile_w4<FMT < 0 ? 0 : FMT>(a, S, a.gu, ring, at, whole ? team : 0, whole ? kFewTeams : 1, xs, xpitch, warp,
                                    lane, acc);
         float* to = red + 16 * t4 + g;
-        to[0] = acc[0];
-        to[8] = acc[1];
-        to[64] = acc[2];
-        to[72] = acc[3];
+        to[0] = kW4Unit<false> * acc[0];
+        to[8] = kW4Unit<false> * acc[1];
+        to[64] = kW4Unit<false> * acc[2];
+        to[72] = kW4Unit<false> * acc[3];
       } else {
         float gate[NQ][4] = {}, up[NQ][4] = {};
         tile_bf16<NQ>(a, S, s ? a.gu : a.gu_s, ring, at, xs, xpitch, warp, lane, gate, up);
@@ -886,7 +886,7 @@ __device__ __forceinline__ void down_w4(const FewArgs& a, FewShared& S, const Fe
   for (int i = 0; i < NI; ++i) {
     float v = sum[i / 2][2 * (i % 2)] + (t4 & 1 ? 0.f : sum[i / 2][2 * (i % 2) + 1]);
     v += __shfl_xor_sync(0xffffffffu, v, 1);
-    if (t4 == 0 || (t4 == 2 && two)) S.out[warp][8 * i + g][token] += v;
+    if (t4 == 0 || (t4 == 2 && two)) S.out[warp][8 * i + g][token] += kW4Unit<false> * v;
   }
 }
 

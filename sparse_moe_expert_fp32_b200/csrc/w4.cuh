@@ -101,6 +101,11 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -112,25 +117,36 @@ __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c
   return r;
 }
 
-// One word of codes -> the four pairs (2 m, 2 m + 1), m = 0..3, of c - 8: exact. A code in the
-// low mantissa bits of 128 (bf16) or 1024 (fp16) is 128 + c or 1024 + c; fp16 has room for the
-// code four bits higher too (1024 + 16 c), which saves a shift.
+// One word of codes -> the four pairs (2 m, 2 m + 1), m = 0..3, of (c - 8) / kW4Unit: exact, and
+// without moving every code to the lowest bits. fp16: a code in the low mantissa bits of 1024 is
+// 1024 + c, one four bits higher 1024 + 16 c. bf16 has no such room, but taken as a bf16 by themselves
+// (subnormal, or of the lowest binade, which goes on in the same steps) the code is c 2^-133 and the one
+// four bits higher c 2^-129; a multiplication by 2^127 or 2^123 brings both to c / 64.
+template <bool F16>
+constexpr float kW4Unit = F16 ? 1.f : 64.f;
 template <bool F16>
 __device__ __forceinline__ uint4 w4_pairs(uint32_t w) {
   uint4 r;
+  const uint32_t v = w >> 8;
   if constexpr (F16) {
-    const uint32_t v = w >> 8;
     r.x = sub_f16x2(and_or(w, 0x000f000fu, 0x64006400u), 0x64086408u);              // - 1032
     r.y = fma_f16x2(and_or(w, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);  // /16 - 72
     r.z = sub_f16x2(and_or(v, 0x000f000fu, 0x64006400u), 0x64086408u);
     r.w = fma_f16x2(and_or(v, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd480d480u);
   } else {
-    r.x = sub_bf16x2(and_or(w, 0x000f000fu, 0x43004300u), 0x43084308u);  // 128 + c - 136
-    r.y = sub_bf16x2(and_or(w >> 4, 0x000f000fu, 0x43004300u), 0x43084308u);
-    r.z = sub_bf16x2(and_or(w >> 8, 0x000f000fu, 0x43004300u), 0x43084308u);
-    r.w = sub_bf16x2(and_or(w >> 12, 0x000f000fu, 0x43004300u), 0x43084308u);
+    r.x = fma_bf16x2(w & 0x000f000fu, 0x7f007f00u, 0xbe00be00u);  // 2^127, -1/8
+    r.y = fma_bf16x2(w & 0x00f000f0u, 0x7d007d00u, 0xbe00be00u);  // 2^123
+    r.z = fma_bf16x2(v & 0x000f000fu, 0x7f007f00u, 0xbe00be00u);
+    r.w = fma_bf16x2(v & 0x00f000f0u, 0x7d007d00u, 0xbe00be00u);
   }
   return r;
+}
+// The same as bf16 pairs of c - 8 itself: 128 + c - 136.
+__device__ __forceinline__ uint4 w4_codes(uint32_t w) {
+  return make_uint4(sub_bf16x2(and_or(w, 0x000f000fu, 0x43004300u), 0x43084308u),
+                    sub_bf16x2(and_or(w >> 4, 0x000f000fu, 0x43004300u), 0x43084308u),
+                    sub_bf16x2(and_or(w >> 8, 0x000f000fu, 0x43004300u), 0x43084308u),
+                    sub_bf16x2(and_or(w >> 12, 0x000f000fu, 0x43004300u), 0x43084308u));
 }
 
 // The scales of a block's four 32-element parts as four bf16: group 32 << shift elements, `s` the

@@ -162,7 +162,7 @@ matvec_w4_kernel(const MvArgs a) {
           for (int i = 0; i < 4; ++i) {
             const int t = 8 * n + 2 * t4 + (i & 1);
             const int64_t row = r0 + 16 * p + 8 * (i >> 1) + g;
-            if (group < a.groups && t < a.T && row < a.N) mv_store<F16>(a, t, row, acc[p][n][i]);
+            if (group < a.groups && t < a.T && row < a.N) mv_store<F16>(a, t, row, acc[p][n][i] * kW4Unit<F16>);
           }
     } else {
 #pragma unroll
@@ -181,7 +181,7 @@ matvec_w4_kernel(const MvArgs a) {
         if (row >= a.N) continue;
         float v = 0.f;
         for (int w = 0; w < a.split; ++w) v += red[((size_t)(w0 + w) * 16 * NP + r % (16 * NP)) * (8 * NT) + t];
-        mv_store<F16>(a, t, row, v);
+        mv_store<F16>(a, t, row, v * kW4Unit<F16>);
       }
       __syncthreads();  // red is read
     }

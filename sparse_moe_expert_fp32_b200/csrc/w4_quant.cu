@@ -218,7 +218,7 @@ dequantize_w4_kernel(const uint8_t* __restrict__ q, const uint16_t* __restrict__
 #pragma unroll
     for (int u = 0; u < kQuantBatch; ++u) {
       if (row[u] >= rows) continue;
-      const uint4 c = w4_pairs<false>(word[u]);  // c - 8 as bf16, exactly
+      const uint4 c = w4_codes(word[u]);  // c - 8 as bf16, exactly
       const uint64_t at = (uint64_t)row[u] * k + b[u] * kW4Block;
       const int n = (int)min((uint32_t)kW4Block, k - b[u] * kW4Block);
       if constexpr (BF16) {
