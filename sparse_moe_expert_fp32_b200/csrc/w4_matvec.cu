@@ -5,8 +5,8 @@
 // Bound by the weight bytes, 1/2 + 2/group each, and close to it by the arithmetic that makes
 // MMA operands of them. A group of warps takes 32 matrix rows (16 if there are few) and splits
 // their 128-element blocks; the fewer rows there are, the more warps a group has, so that small
-// matrices still spread over all SMs without a second launch. The codes are loaded straight to
-// registers, a block ahead; x is staged in shared memory. The MMA's A is 16
+// matrices still spread over all SMs without a second launch. The codes come two blocks ahead; x is
+// staged in shared memory. The MMA's A is 16
 // matrix rows, made in registers, its columns are 8 rows of x. The codes enter as exact
 // integers; the fp32 sum over a scale group is multiplied by the scale and added to the running
 // fp32 sums, so no product or weight is rounded.
@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kMvWarps = 16;
 constexpr int kMvThreads = kMvWarps * 32;
-constexpr int kMvXBytes = 163840;  // staged x; what is longer comes in K chunks
+constexpr int kMvXBytes = 131072;  // staged x; what is longer comes in K chunks
 
 struct MvArgs {
   const uint16_t* x;
@@ -36,22 +36,18 @@ struct MvArgs {
   int T, kc, split, y_f32;  // split: warps of a row group
 };
 
-// A block of 16 NP rows: this lane's rows 8 i + g.
-template <int NP>
-struct MvTile {
-  uint4 w[2 * NP];
-  uint2 s[2 * NP];
-};
-
-template <int SHIFT, int NP>
-__device__ __forceinline__ void mv_load(MvTile<NP>& m, const uint8_t* q, const uint16_t* s, const int (&row)[2 * NP],
-                                        int64_t row_bytes, int64_t row_scales, int64_t b) {
-#pragma unroll
-  for (int i = 0; i < 2 * NP; ++i) {
-    m.w[i] = ld_stream_v4(q + row[i] * row_bytes + b * kW4BlockBytes);
-    m.s[i] = w4_block_scales(s + row[i] * row_scales, (int)b, SHIFT);
-  }
+// The codes come through a ring of kMvDepth blocks in shared memory, a warp's own: a lane copies the 16
+// bytes of its rows 8 i + g that it reads itself, so its own waits are all there is to wait for.
+constexpr int kMvDepth = 3;
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <bool F16, int SHIFT, int NT, int NP>
 __device__ __forceinline__ void mv_block(const uint4 (&w)[2 * NP], const uint2 (&s)[2 * NP], uint32_t xp, int pitch,
@@ -100,7 +96,9 @@ matvec_w4_kernel(const MvArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const int pitch = 2 * a.kc + 64;  // 64 mod 128: two tokens' 64-byte reads share no bank
-  float* red = reinterpret_cast<float*>(smem + (size_t)a.T * pitch);  // [warp][row][NT * 8]
+  constexpr int ring = kMvDepth * 2 * NP * 512;  // bytes of a warp
+  uint8_t* behind = smem + (size_t)a.T * pitch;
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(behind) + warp * ring + 16 * lane;
   const uint32_t xs = (uint32_t)__cvta_generic_to_shared(smem) + g * pitch + 16 * t4;
   const int part = warp % a.split, per_cta = kMvWarps / a.split;
   int tok[NT];
@@ -120,38 +118,67 @@ matvec_w4_kernel(const MvArgs a) {
       const int kn = (int)min((int64_t)a.kc, a.K - k0);
       const int nb = (int)w4_blocks(kn);
       const int64_t b0 = k0 / kW4Block;
-      MvTile<NP> cur, next;
-      const bool work = group < a.groups && part < nb;
-      if (work) mv_load<SHIFT, NP>(cur, q, s, row, a.row_bytes, a.row_scales, b0 + part);
+      const bool work = group < a.groups;
+      uint2 sc[2 * NP], sn[2 * NP];  // scales, a block ahead
+      auto fetch = [&](int b, int slot) {  // (a group without copies where there is no such block)
+        if (work && b < nb)
+#pragma unroll
+          for (int i = 0; i < 2 * NP; ++i)
+            copy16(mine + (slot * 2 * NP + i) * 512, q + row[i] * a.row_bytes + (b0 + b) * kW4BlockBytes);
+        copy_commit();
+      };
+      auto fetch_scales = [&](int b) {
+#pragma unroll
+        for (int i = 0; i < 2 * NP; ++i) sn[i] = w4_block_scales(s + row[i] * a.row_scales, (int)(b0 + b), SHIFT);
+      };
+#pragma unroll
+      for (int d = 0; d < kMvDepth - 1; ++d) fetch(part + d * a.split, d);
+      if (work && part < nb) fetch_scales(part);
       if (a.kc < a.K || first == (int64_t)blockIdx.x * per_cta) {
         __syncthreads();  // every warp is done with the last chunk of x
-        // x, zeros up to whole blocks: 16 bytes a thread where the rows are aligned
-        const int64_t row_elems = (int64_t)nb * kW4Block;
-        const bool vec = ((reinterpret_cast<uintptr_t>(a.x) | (uint64_t)(2 * a.ldx)) & 15u) == 0 && kn % 8 == 0;
-        if (vec) {
-          const int cols = (int)(row_elems / 8);
-          for (int i = tid; i < a.T * cols; i += kMvThreads) {
-            const int t = i / cols, c = i - t * cols;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (8 * c < kn) v = ld_v4(a.x + t * a.ldx + k0 + 8 * c);
-            *reinterpret_cast<uint4*>(smem + (size_t)t * pitch + 16 * c) = v;
+        // x, zeros up to whole blocks; warp by warp, so that a thread's loads are all in flight
+        const int cols = nb * kW4Block;
+        const uint32_t x0 = (uint32_t)__cvta_generic_to_shared(smem);
+        if (((reinterpret_cast<uintptr_t>(a.x) | (uint64_t)(2 * a.ldx)) & 15u) == 0 && kn % 8 == 0) {
+          for (int t = 0; t < a.T; ++t) {
+            const uint16_t* from = a.x + t * a.ldx + k0;
+            for (int k = 8 * tid; k < cols; k += 8 * kMvThreads)
+              copy16_or_zero(x0 + t * pitch + 2 * k, from + (k < kn ? k : 0), k < kn);
           }
+          copy_commit();
+          copy_wait<0>();
         } else {
-          for (int64_t i = tid; i < a.T * row_elems; i += kMvThreads) {
-            const int t = (int)(i / row_elems), k = (int)(i - t * row_elems);
-            *reinterpret_cast<uint16_t*>(smem + (size_t)t * pitch + 2 * k) =
-                k < kn ? __ldg(a.x + t * a.ldx + k0 + k) : (uint16_t)0;
+          constexpr int batch = 8;
+          for (int t = 0; t < a.T; ++t) {
+            const uint16_t* from = a.x + t * a.ldx + k0;
+            uint16_t* to = reinterpret_cast<uint16_t*>(smem + (size_t)t * pitch);
+            for (int k = tid; k < cols; k += batch * kMvThreads) {
+              uint16_t v[batch];
+#pragma unroll
+              for (int i = 0; i < batch; ++i)
+                v[i] = k + i * kMvThreads < kn ? __ldg(from + k + i * kMvThreads) : (uint16_t)0;
+#pragma unroll
+              for (int i = 0; i < batch; ++i)
+                if (k + i * kMvThreads < cols) to[k + i * kMvThreads] = v[i];
+            }
           }
         }
         __syncthreads();
       }
-      if (work)
-        for (int b = part; b < nb; b += a.split) {
-          const bool more = b + a.split < nb;
-          if (more) mv_load<SHIFT, NP>(next, q, s, row, a.row_bytes, a.row_scales, b0 + b + a.split);
-          mv_block<F16, SHIFT, NT, NP>(cur.w, cur.s, xs + 256 * b, pitch, tok, acc);
-          if (more) cur = next;
+      for (int b = part, slot = 0; b < nb; b += a.split, slot = (slot + 1) % kMvDepth) {
+        fetch(b + (kMvDepth - 1) * a.split, (slot + kMvDepth - 1) % kMvDepth);
+        copy_wait<kMvDepth - 1>();
+        if (!work) continue;
+        uint4 w[2 * NP];
+#pragma unroll
+        for (int i = 0; i < 2 * NP; ++i) {
+          w[i] = lds_v4(mine + (slot * 2 * NP + i) * 512);
+          sc[i] = sn[i];
         }
+        if (b + a.split < nb) fetch_scales(b + a.split);
+        mv_block<F16, SHIFT, NT, NP>(w, sc, xs + 256 * b, pitch, tok, acc);
+      }
+      copy_wait<0>();  // the next chunk starts with an empty ring
     }
     if (a.split == 1) {
 #pragma unroll
@@ -165,13 +192,16 @@ matvec_w4_kernel(const MvArgs a) {
             if (group < a.groups && t < a.T && row < a.N) mv_store<F16>(a, t, row, acc[p][n][i] * kW4Unit<F16>);
           }
     } else {
+      // the sums of a warp [row][NT * 8] take the place of its ring
+      static_assert(16 * NP * 8 * NT * 4 <= ring, "");
+      float* red = reinterpret_cast<float*>(behind + warp * ring);
 #pragma unroll
       for (int p = 0; p < NP; ++p)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float2*>(red + ((size_t)warp * 16 * NP + 16 * p + 8 * h + g) * (8 * NT) + 8 * n + 2 * t4) =
+            *reinterpret_cast<float2*>(red + (16 * p + 8 * h + g) * (8 * NT) + 8 * n + 2 * t4) =
                 make_float2(acc[p][n][2 * h], acc[p][n][2 * h + 1]);
       __syncthreads();
       const int rows = per_cta * 16 * NP;
@@ -180,7 +210,8 @@ matvec_w4_kernel(const MvArgs a) {
         const int64_t row = first * (16 * NP) + r;
         if (row >= a.N) continue;
         float v = 0.f;
-        for (int w = 0; w < a.split; ++w) v += red[((size_t)(w0 + w) * 16 * NP + r % (16 * NP)) * (8 * NT) + t];
+        for (int w = 0; w < a.split; ++w)
+          v += reinterpret_cast<const float*>(behind + (w0 + w) * ring)[r % (16 * NP) * (8 * NT) + t];
         mv_store<F16>(a, t, row, v * kW4Unit<F16>);
       }
       __syncthreads();  // red is read
@@ -211,7 +242,7 @@ cudaError_t launch_matvec_w4(int T, int64_t N, int64_t K, int shift, const uint1
   while (a.split < kMvWarps && a.split < nb && a.groups * a.split * 2 <= (int64_t)sms * kMvWarps) a.split *= 2;
   const int per_cta = kMvWarps / a.split;
   const int64_t ctas = (a.groups + per_cta - 1) / per_cta;
-  const size_t smem = (size_t)T * (2 * a.kc + 64) + (a.split > 1 ? (size_t)kMvWarps * 16 * np * nt * 8 * sizeof(float) : 0);
+  const size_t smem = (size_t)T * (2 * a.kc + 64) + (size_t)kMvWarps * kMvDepth * 2 * np * 512;
   const void* fn = f16 ? (shift == 0 ? mv_kernel<true, 0>(nt, np) : shift == 1 ? mv_kernel<true, 1>(nt, np) : mv_kernel<true, 2>(nt, np))
                        : (shift == 0 ? mv_kernel<false, 0>(nt, np) : shift == 1 ? mv_kernel<false, 1>(nt, np) : mv_kernel<false, 2>(nt, np));
   static std::atomic<uint64_t> done[2][3][2][2];
