@@ -24,6 +24,7 @@
 #include <float.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "moe_internal.h"
 #include "sm100_ptx.cuh"
@@ -66,6 +67,7 @@ struct FewArgs {
   uint32_t* sync;   // barrier counters: zero between calls
   uint32_t* status;
   int T, H, E, k, I, Is, ldh, ldl, shift;
+  uint32_t per_tile;  // 2^32 over the tiles of an expert, rounded up
   FewChunks gu, gu_s, dn, dn_s;  // gate|up and down matrices, routed and shared
   int rows;                      // output rows of a pass
   int stages, stage_bytes;
@@ -194,6 +196,10 @@ struct Place {
   __device__ void skip(int n, int stages) {
     i += n;
     for (cur.s += n; cur.s >= stages; cur.s -= stages) cur.parity ^= 1u;
+  }
+  __device__ void back(int n, int stages) {
+    i -= n;
+    for (cur.s -= n; cur.s < 0; cur.s += stages) cur.parity ^= 1u;
   }
 };
 
@@ -520,7 +526,7 @@ __device__ __forceinline__ void tile_bf16(const FewArgs& a, FewShared& S, const 
     uint32_t wp = st + 64 * g + 16 * t4 + 512 * wt, xp = xg + (b0 + wt) * 64;
     const uint32_t up_at = 512 * ch.cb;
     float dg[NQ][4] = {}, du[NQ][4] = {};
-#pragma unroll 5
+#pragma unroll 2
     for (int b = wt; b < nb; b += kFewTeam, wp += 512 * kFewTeam, xp += 64 * kFewTeam) {
       const uint4 wg = lds_v4(wp), wu = lds_v4(wp + up_at);
 #pragma unroll
@@ -605,26 +611,34 @@ __device__ __forceinline__ void fold(const float (&d)[4], bool low, float& v0, f
   v1 += __shfl_xor_sync(0xffffffffu, v1, 2);
 }
 
-// Tiles up to tile `end`; the teams take them in turn. `at`: the first tile's first stage, on return
-// the one behind the last tile's.
+// The tiles first, first + grid, ... of the shared expert or (`routed`) of the chosen ones, `count` of
+// them; the teams take them in turn. `at`: the first tile's first stage, on
+// return the one behind the last tile's.
 template <int FMT, int NQ>
 __device__ __forceinline__ void gate_up_tiles(const FewArgs& a, FewShared& S, uint32_t xs, int xpitch,
-                                              uint32_t ring, Place& at, Tiles& tile, int& turn, int end) {
+                                              uint32_t ring, Place& at, bool routed, int first, int count, int& turn) {
+  constexpr bool W4 = FMT >= 0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const int team = warp / kFewTeam, wt = warp & (kFewTeam - 1);
-  int buf = 0;
-  for (; tile.u < end; tile.next()) {
-    tile.settle(a.Is / 8, a.I / 8);
-    const int s = tile.s, c0 = 8 * tile.c;
-    const int n = s ? a.gu.n : a.gu_s.n;
-    // a tile with so many chunks that two of them do not fit in the ring is taken by both teams
-    const bool whole = FMT >= 0 && s && 2 * n > a.stages, mine = whole || turn == team;
-    if (!whole) turn = turn + 1 == kFewTeams ? 0 : turn + 1;
-    if (mine) {
+  const FewChunks& chunks = routed ? a.gu : a.gu_s;
+  // a tile with so many chunks that two of them do not fit in the ring is taken by all teams
+  const bool whole = W4 && 2 * chunks.n > a.stages;
+  const int step = whole ? 1 : kFewTeams;
+  int buf = 0, i = whole ? 0 : team >= turn ? team - turn : team - turn + kFewTeams;
+  at.skip(i * chunks.n, a.stages);
+  for (; i < count; i += step, at.skip(step * chunks.n, a.stages)) {
+    const int u = first + i * gridDim.x;
+    int s = 0, c0 = 8 * u;
+    if (routed) {
+      const int q = (int)__umulhi((uint32_t)u, a.per_tile);  // u / (I / 8), or one more
+      s = 1 + q - (q * (a.I / 8) > u);
+      c0 -= (s - 1) * a.I;
+    }
+    {
       float* red = S.red[buf][team][wt];  // [gate, up][token][channel]
-      if (FMT >= 0 && s) {
+      if constexpr (W4) {
         float acc[4] = {};
-        tile_w4<FMT < 0 ? 0 : FMT>(a, S, a.gu, ring, at, whole ? team : 0, whole ? kFewTeams : 1, xs, xpitch, warp,
+        tile_w4<FMT < 0 ? 0 : FMT>(a, S, chunks, ring, at, whole ? team : 0, whole ? kFewTeams : 1, xs, xpitch, warp,
                                    lane, acc);
         float* to = red + 16 * t4 + g;
         to[0] = kW4Unit<false> * acc[0];
@@ -633,7 +647,7 @@ __device__ __forceinline__ void gate_up_tiles(const FewArgs& a, FewShared& S, ui
         to[72] = kW4Unit<false> * acc[3];
       } else {
         float gate[NQ][4] = {}, up[NQ][4] = {};
-        tile_bf16<NQ>(a, S, s ? a.gu : a.gu_s, ring, at, xs, xpitch, warp, lane, gate, up);
+        tile_bf16<NQ>(a, S, chunks, ring, at, xs, xpitch, warp, lane, gate, up);
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
           float g0, g1, v0, v1;
@@ -648,7 +662,7 @@ __device__ __forceinline__ void gate_up_tiles(const FewArgs& a, FewShared& S, ui
       else ptx::bar_sync(kBarTeam + team, 32 * kFewTeam);
       if (wt >> 1 == buf && (!whole || team == 0)) {  // a pair of the team's warps finishes the tile, the other pair its next one
         const int at64 = tid & 63, t = at64 >> 3, c = at64 & 7;
-        const uint32_t m = s ? S.act_mask[s] : (1u << a.T) - 1u;
+        const uint32_t m = routed ? S.act_mask[s] : (1u << a.T) - 1u;
         if ((m >> t) & 1u) {
           float gate = 0.f, up = 0.f;
           for (int q = whole ? 0 : team; q < (whole ? kFewTeams : team + 1); ++q)
@@ -657,8 +671,8 @@ __device__ __forceinline__ void gate_up_tiles(const FewArgs& a, FewShared& S, ui
               gate += S.red[buf][q][w][at64];
               up += S.red[buf][q][w][64 + at64];
             }
-          const int pair = s ? S.act_pair[s] + __popc(m & ((1u << t) - 1u)) : t;
-          const float h = __fdividef(gate * up * (s ? S.pair_w[pair] : 1.f), 1.f + expf(-gate));
+          const int pair = routed ? S.act_pair[s] + __popc(m & ((1u << t) - 1u)) : t;
+          const float h = __fdividef(gate * up * (routed ? S.pair_w[pair] : 1.f), 1.f + expf(-gate));
           // three truncated pieces: 8 + 8 + 8 significant bits, h exactly (an infinity or NaN in
           // the first alone)
           const uint32_t hb = __float_as_uint(h);
@@ -675,8 +689,9 @@ __device__ __forceinline__ void gate_up_tiles(const FewArgs& a, FewShared& S, ui
       }
       buf ^= 1;  // the team's next tile uses the other half: one barrier a tile is enough
     }
-    at.skip(n, a.stages);
   }
+  at.back((i - count) * chunks.n, a.stages);
+  if (!whole) turn = (turn + count) % kFewTeams;
 }
 
 // ---------------------------------------------------------------- down
@@ -789,7 +804,7 @@ __device__ __forceinline__ void down_bf16(const FewArgs& a, FewShared& S, uint32
     x[n] = make_uint4(0u, 0u, 0u, 0u);
   }
   float sum[N][NI][4] = {};
-#pragma unroll 5
+#pragma unroll 2
   for (int b = wt; b < nb; b += step, wp += 64 * step * a.rows) {
     uint2 y[N];
 #pragma unroll
@@ -947,12 +962,7 @@ __device__ __forceinline__ void down_pass(const FewArgs& a, FewShared& S, uint32
                         wt & (share - 1), share, warp, lane);
     release();
   }
-  at.i -= j - end;  // back to the first stage of the next pass
-  at.cur.s -= j - end;
-  if (at.cur.s < 0) {
-    at.cur.s += a.stages;
-    at.cur.parity ^= 1u;
-  }
+  at.back(j - end, a.stages);  // to the first stage of the next pass
   turn = (turn + end) % kFewTeams;
   unit = wrap(routed + pairs * a.dn.n);
 }
@@ -1135,16 +1145,24 @@ __device__ void consume(const FewArgs& a, FewShared& S, uint8_t* xs, int xpitch,
   grid_arrive(a.sync);
 
   const uint32_t xs_at = ptx::smem_u32(xs), ring_at = ptx::smem_u32(ring);
-  Tiles tile;
-  tile.begin();
-  int end = a.Is / 8;  // the shared expert's gate|up tiles need no routing
+  // tiles b, b + grid, ...: of the shared expert (they need no routing), then of the chosen ones; bf16:
+  // by the same code, which is warm by then
+  const int grid = gridDim.x;
+  int first = blockIdx.x, tiles = a.Is / 8;
   for (int pass = 0; pass < 2; ++pass) {
     if (pass) {
       route(a, S, ring, warp, lane);
-      end += (S.n_act - 1) * (a.I / 8);
+      tiles = (S.n_act - 1) * (a.I / 8);
     }
-    if (a.T <= 4) gate_up_tiles<FMT, 1>(a, S, xs_at, xpitch, ring_at, at, tile, turn, end);
-    else gate_up_tiles<FMT, 2>(a, S, xs_at, xpitch, ring_at, at, tile, turn, end);
+    const int count = max((tiles - first + grid - 1) / grid, 0);
+    auto run = [&](auto fmt) {
+      constexpr int F = decltype(fmt)::value;
+      if (a.T <= 4) gate_up_tiles<F, 1>(a, S, xs_at, xpitch, ring_at, at, pass, first, count, turn);
+      else gate_up_tiles<F, 2>(a, S, xs_at, xpitch, ring_at, at, pass, first, count, turn);
+    };
+    if (FMT >= 0 && pass) run(std::integral_constant<int, FMT>{});
+    else run(std::integral_constant<int, -1>{});
+    first += count * grid - tiles;
   }
 
   // h of this CTA is written (for bulk copies to read); that of the others comes through the ring
@@ -1290,6 +1308,7 @@ cudaError_t launch_few_layer(const moe_shape& s, const Layout& L, char* ws, cons
   a.ldl = (s.E + 2) / 2 * 2;
   a.sync = reinterpret_cast<uint32_t*>(ws + L.status) + kFewSyncWord;
   a.status = reinterpret_cast<uint32_t*>(ws + L.status);
+  a.per_tile = (uint32_t)(((1ull << 32) + s.I / 8 - 1) / (s.I / 8));
   a.T = s.T; a.H = s.H; a.E = s.E; a.k = s.k; a.I = s.I; a.Is = s.Is;
 
   const int cap = kFewRows;
