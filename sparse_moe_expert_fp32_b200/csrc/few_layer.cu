@@ -1315,9 +1315,10 @@ cudaError_t launch_few_layer(const moe_shape& s, const Layout& L, char* ws, cons
   const int most_rows = (s.H + sms - 1) / sms, passes = (most_rows + cap - 1) / cap;
   a.rows = (most_rows + passes - 1) / passes;
   const int x_bytes = s.T * (2 * s.H + 64);
-  // bf16: six stages of 24 KB, which keep a 20-block chunk of a gate|up tile or of a block's output rows;
-  // 4-bit: twice as many of half the size. Smaller and then fewer where x leaves less room.
-  const int most_bytes = 24576, least_bytes = q ? 7168 : 15360;
+  // Six stages of 24 KB; where x leaves less room, smaller ones, below 15 KB fewer of them: a stage costs
+  // its team some 700 clocks besides its weights. (8 tokens of H = 8192, I = 2048, 4-bit weights: six
+  // stages of 13 KB 484 us, five of 16 KB 433 us, four of 20 KB 450 us.)
+  const int most_bytes = 24576, least_bytes = 15360;
   for (a.stages = 6;; --a.stages) {
     for (a.stage_bytes = most_bytes;; a.stage_bytes -= 1024) {
       a.gu_s = few_chunks(s.H, 16, false, 0, a.stage_bytes, 32);
@@ -1338,9 +1339,11 @@ cudaError_t launch_few_layer(const moe_shape& s, const Layout& L, char* ws, cons
   a.h_bytes = ((int)kFewSmem - (int)kFewSharedBytes - a.stages * a.stage_bytes) / 128 * 128;
   a.units = std::min(a.h_bytes / a.unit, 64);
   a.slot = (a.rows * 64 * a.dn.cb + 127) / 128 * 128 + (a.rows * a.dn.sc + 127) / 128 * 128;
-  // experts of a stage: 1, 2 or 4, so that each has as many of the team's warps
+  // experts of a stage: 1, 2 or 4, so that each has as many of the team's warps; bf16: and so few that a
+  // warp's share of one is a chain of at most 8 instructions, as everywhere
   const int fit = std::min(a.stage_bytes / a.slot, a.units / s.T);
   a.group = a.dn.n > 1 || fit < 2 ? 1 : fit < kFewTeam ? 2 : kFewTeam;
+  while (!q && a.group * a.dn.cb > 8 * kFewTeam) a.group /= 2;
 
   FewMaps m;
   bool ok = few_weight_map(&m.gu_s, w.ws_gate_up, s.Is, a.gu_s, 2 * (uint64_t)s.H, 2, 1, 8) &&

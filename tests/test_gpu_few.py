@@ -1,9 +1,9 @@
 """The few-token layer on the GPU, with bf16 and with 4-bit experts, against the layer in 64 bits.
 
 Tolerance (u = 2^-24), from the kernel's arithmetic: products are exact; a tensor instruction adds 16 of
-them to its accumulator with at most 2 u of the magnitudes lost an addition, at most 6 instructions share
-an accumulator (6 * 17 * 2 u = 204 u), and a row's parts are added in fp32 (at most K / 32 + 36 additions
-of u each). With c(K) = 240 + K / 32:
+them to its accumulator with at most 2 u of the magnitudes lost an addition, at most 8 instructions share
+an accumulator (8 * 17 * 2 u = 272 u), and a row's parts are added in fp32 (at most K / 32 + 38 additions
+of u each). With c(K) = 310 + K / 32:
   |dg| <= c(H) u G, |du| <= c(H) u Up     (G, Up: the sums of |x w|)
   |dh| <= 1.1 |u| |dg| + |silu(g)| |du| + 16 u |h|     (|silu'| < 1.1; exp, division, products; p)
   |dout| <= sum_e |Wd| (dh + c(K_all) u |h|)            (h with its routing weight in it)
@@ -97,7 +97,7 @@ def _reference(s, x, w, gate_up, down):
     gap = top[:, s.k - 1] - top[:, s.k] if s.k < s.E else torch.full((s.T,), float("inf"), device="cuda",
                                                                     dtype=torch.float64)
     n_all = (s.T * s.k * s.I + s.Is) / 32
-    ch, cd = (240 + s.H / 32) * U, (240 + n_all) * U
+    ch, cd = (310 + s.H / 32) * U, (310 + n_all) * U
     out, tol = torch.zeros_like(x), torch.zeros_like(x)
 
     def expert(t, wgu, wd, weight):
@@ -117,7 +117,7 @@ def _reference(s, x, w, gate_up, down):
     wgu, wd = w["ws_gate_up"].double(), w["ws_down"].double()
     sg = torch.sigmoid(x @ w["w_shared_gate"].double())
     # the gate's own sum: |d sigmoid| <= |dz| / 4 and sigmoid >= its value; relative |dz|
-    dz = (240 + s.H / 32) * U * (x.abs() @ w["w_shared_gate"].double().abs())
+    dz = (310 + s.H / 32) * U * (x.abs() @ w["w_shared_gate"].double().abs())
     for t in range(s.T):
         expert(t, wgu, wd, sg[t])
         n = wgu.shape[0] // 2
@@ -364,8 +364,8 @@ def test_4_bit_set_in_a_row():
     out = torch.empty(64, 256, device="cuda")
     moe.moe_layer_forward(big, xb, back, out, moe.alloc_workspace(big))
     ref = _reference(s, x, back, lambda e: back["w_gate_up"][e].double(), lambda e: back["w_down"][e].double())
-    # tol is 240 u and more of the magnitudes: 2^-8 is 2^16 u
-    assert ((got[0] - out[:4]).double().abs() <= ref[4] * (3 * 2.0 ** 16 / 240)).all()
+    # tol is 310 u and more of the magnitudes: 2^-8 is 2^16 u
+    assert ((got[0] - out[:4]).double().abs() <= ref[4] * (3 * 2.0 ** 16 / 310)).all()
     e = int(got[1][0, 0])
     y = torch.empty(4, 2 * 128, device="cuda")
     moe.moe_matvec_w4(x, q["q_gate_up"][e], q["s_gate_up"][e], y, 32)
