@@ -10,17 +10,32 @@
 //      output by whole experts).
 //   2. shared expert's gate|up tiles, which need no routing, while the barrier fills.
 //   -- barrier: all logits are there. Every CTA selects the top-k of all tokens for itself.
-//   3. gate|up tiles of the chosen experts: 8 channels (8 gate rows and the 8 up rows: one m16
-//      tile, so a thread holds the gate and the up sum of the same channel) by the full hidden
-//      size, split over the CTA's 16 warps. The epilogue multiplies h = SiLU(gate) up by the
-//      routing weight and stores it as three bf16 pieces (truncations; exactly fp32's 24 bits).
+//   3. gate|up tiles of the chosen experts: 8 channels (8 gate rows and the 8 up rows) by the full
+//      hidden size, by a team of four of the twelve consumer warps, which split K. The epilogue
+//      multiplies h = SiLU(gate) up by the routing weight and stores it as three bf16 pieces
+//      (truncations; exactly fp32's 24 bits).
 //   -- barrier: all of h is there.
-//   4. down. A CTA owns H / grid output rows and runs through all chosen experts, accumulating
-//      in registers: the routing weights are in h, so the weighted combine is the sum over the
-//      experts and nothing is added atomically. The result does not depend on timing.
-// The MMA columns are the tokens themselves: a tile multiplies all tokens, and the columns of
-// tokens not routed to its expert are dropped (not multiplied by zero, so that an infinite or
-// NaN weight stays within the tokens that chose its expert).
+//   4. down. A CTA owns H / grid output rows and runs through all chosen experts, a stage's blocks
+//      of K split over a team; every warp keeps sums of its own, added up at the end: the routing
+//      weights are in h, so the weighted combine is the sum over the experts and nothing is added
+//      atomically. The result does not depend on timing.
+// A tile multiplies all tokens (they are the MMA's columns), and the columns of tokens not routed to
+// its expert are dropped, not multiplied by zero, so that an infinite or NaN weight stays within the
+// tokens that chose its expert.
+//
+// mma.sync rather than tcgen05: a weight is used 1 to 8 times, so its bytes are the bound, and what
+// counts is how few instructions make operands of them. bf16 weights are the A of m16n8k16 just as a
+// 16-byte load leaves them (mma_rows); a tcgen05 tile would have 128 rows of one expert and leave
+// 7/8 of its columns empty, and 4-bit weights would go back to shared memory as bf16 first.
+//
+// Measured on one B200, weights not in L2, H = 2560, E = 512, k = 10, I = Is = 640 unless said; the
+// floor is the weights' bytes at the measured copy rate of 6.56 TB/s:
+//   bf16   1 token 35 us (floor 17), 8 tokens 146 us (115: 5.1 TB/s)
+//          4 tokens, H = 8192, E = 64, I = Is = 2048, some 26 experts chosen: 446 us (415: 6.1 TB/s)
+//   4-bit  1 token 29 us (6.5), 5 tokens 66 us (21); 8 tokens, H = 8192, I = 2048: 439 us (204)
+// bf16 is bound by HBM with about 10 us before the first expert's weights can be asked for (the router,
+// a barrier, the choice) and 4 us at the second barrier; 4-bit weights by the instructions that unpack
+// them (some 28 for each MMA, 1.6 of 4 a clock and SM), which take twice the time of their bytes.
 #include <float.h>
 
 #include <algorithm>
@@ -1136,7 +1151,7 @@ template <int FMT>
 __device__ void consume(const FewArgs& a, FewShared& S, uint8_t* xs, int xpitch, uint8_t* ring) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Place at{0, {0, 0u}};
-  int turn = 0;  // the team that takes the next tile; down: the first warp of the next stage's group
+  int turn = 0;  // the team that takes the next tile or stage
   for (int e = tid; e < a.E; e += kFewThreads) S.mask[e] = 0;
   if (tid < kFewMaxT) S.sgate[tid] = 0.f;
   if (a.T == 1) router_logits<1>(a, S, xs, xpitch, ring, at);
@@ -1182,7 +1197,7 @@ __device__ void consume(const FewArgs& a, FewShared& S, uint8_t* xs, int xpitch,
   }
 }
 
-// Warp 16 feeds weights, warp 17 h; one thread of each.
+// The warp behind the consumers feeds weights, the last one h; one thread of each.
 template <int FMT>
 __device__ void feed(const FewArgs& a, const FewMaps& m, FewShared& S, uint8_t* ring, uint8_t* xs, int xpitch) {
   const int lane = threadIdx.x & 31;

@@ -9,8 +9,8 @@
 // 16 uses, so the kernels are bound by the weight bytes, and a tensor instruction is only the
 // cheapest way to spend them (a tcgen05 tile would need the dequantised weights written back to
 // shared memory, four times the codes' bytes). Its operands are register quads (A) and pairs (B)
-// that have to be consecutive, and a move costs as much as any other instruction, so both uses
-// below take them as they come out of one load. A thread reads 16 bytes of one weight row: lane
+// that have to be consecutive, and a move costs as much as any other instruction, so they are taken
+// as they come out of one load. A thread reads 16 bytes of one weight row: lane
 // 4 g + t the quarter t of row g. Since a sum over K may run in any order, a word of codes, an
 // eighth of a 32-element part of one scale group, becomes four consecutive pairs of elements.
 #pragma once
