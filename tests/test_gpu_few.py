@@ -10,6 +10,8 @@ of u each). With c(K) = 310 + K / 32:
 where the routing weight itself is within 16 u (exp and a sum of at most 32).
 Expert ids have to be equal: the logits' sums are 64-bit on both sides.
 """
+import random
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -146,6 +148,35 @@ def test_layer(name, form):
     s, x, w = _layer(SHAPES[name], seed=len(name))
     experts, gu, dn = _banks(s, w, FORMS[form])
     _check(_run(s, x, w, experts), _reference(s, x, w, gu, dn))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", sorted(FORMS))
+@pytest.mark.parametrize("shape", [
+    (8, 8192, 9, 3, 1088, 320),    # few and small stages; a row of 8.5 blocks of 128
+    (2, 32768, 3, 2, 192, 64),     # many passes of output rows
+    (5, 4160, 30, 7, 704, 448),    # rows and half blocks that divide nothing
+    (8, 2560, 40, 10, 640, 640),   # two experts a stage, or one for want of units of h
+    (1, 128, 300, 32, 64, 64),     # one output row a block, four experts a stage
+    (6, 64, 1024, 32, 64, 64),     # fewer output rows than blocks
+    (1, 2560, 11, 10, 64, 4096),   # a shared expert deeper than the routed ones
+], ids=str)
+def test_layer_where_the_stages_change_shape(shape, form):
+    s, x, w = _layer(shape, seed=sum(shape))
+    experts, gu, dn = _banks(s, w, FORMS[form])
+    _check(_run(s, x, w, experts), _reference(s, x, w, gu, dn))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seed", range(12))
+def test_layer_of_drawn_shapes(seed):
+    r = random.Random(seed)
+    T, E = r.randint(1, 8), r.choice([1, 5, 40, 130])
+    shape = (T, 64 * r.randint(1, 60), E, r.randint(1, min(E, 32)), 64 * r.randint(1, 18), 64 * r.randint(1, 18))
+    s, x, w = _layer(shape, seed=seed, bias=r.random() < 0.5)
+    for form in ("bf16", r.choice(["w4_32", "w4_64", "w4_128"])):
+        experts, gu, dn = _banks(s, w, FORMS[form])
+        _check(_run(s, x, w, experts), _reference(s, x, w, gu, dn))
 
 
 @pytest.mark.gpu

@@ -129,6 +129,26 @@ def test_quantize_a_bank_leaves_the_rest_alone():
     assert (qbuf[12 * nb:] == 0xA5).all() and (sbuf[12 * ns:] == 9).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,K", [(1, 1), (3, 7), (5, 130), (4, 257), (2, 1023), (130, 641)])
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_ragged_rows_stay_within_their_buffers(rows, K, dt):
+    w = _matrix(rows, K, K).cuda()
+    raw = torch.full((rows * K + 64,), float("nan"), dtype=BF16, device="cuda")  # behind w: must not get into it
+    raw[:rows * K] = w.view(-1)
+    nb, ns = moe.moe_w4_row_bytes(K), moe.moe_w4_row_scales(K, 32)
+    qbuf = torch.full((rows * nb + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+    sbuf = torch.full((rows * ns + 8,), 9.0, dtype=BF16, device="cuda")
+    moe.moe_quantize_w4(raw[:rows * K].view(rows, K), qbuf[:rows * nb], sbuf[:rows * ns], 32)
+    q, s = qbuf[:rows * nb].view(rows, nb), sbuf[:rows * ns].view(rows, ns)
+    codes, scales = oracle.quantize_w4_rows(_bits(w), 32)
+    assert np.array_equal(q.cpu().numpy(), oracle.pack_w4_rows(codes))
+    back = torch.full((rows * K + 64,), 5.0, dtype=dt, device="cuda")
+    moe.moe_dequantize_w4(q, s, back[:rows * K].view(rows, K), 32)
+    assert torch.equal(back[:rows * K].view(rows, K).double(), _dense(q, s, K, 32).to(dt).double())
+    assert (back[rows * K:] == 5).all() and (qbuf[rows * nb:] == 0xA5).all() and (sbuf[rows * ns:] == 9).all()
+
+
 # ------------------------------------------------------------------------- product
 
 def _check(x, q, s, K, group, y, ref_w=None):
@@ -148,7 +168,8 @@ def _check(x, q, s, K, group, y, ref_w=None):
 @pytest.mark.parametrize("T,N,K,group", [
     (1, 1, 1, 32), (1, 16, 64, 32), (2, 17, 127, 32), (3, 147, 129, 64), (8, 149, 128, 128), (9, 33, 640, 32),
     (16, 2560, 640, 64), (5, 4099, 2501, 64), (1, 5000, 2560, 32), (7, 300, 8192, 128), (16, 65, 4225, 32),
-    (16, 9500, 256, 128), (4, 64, 16500, 128), (16, 600, 9000, 64), (1, 150000, 64, 32)])
+    (16, 9500, 256, 128), (4, 64, 16500, 128), (16, 600, 9000, 64), (1, 150000, 64, 32),
+    (15, 80001, 320, 32), (13, 700, 13001, 128), (1, 40, 70000, 64)])
 def test_matvec(T, N, K, group, xt, yt):
     g = torch.Generator().manual_seed(T * 7 + N + K)
     x = torch.randn(T, K, generator=g).to(xt).cuda()
