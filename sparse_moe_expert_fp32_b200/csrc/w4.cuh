@@ -121,7 +121,9 @@ __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c
 // without moving every code to the lowest bits. fp16: a code in the low mantissa bits of 1024 is
 // 1024 + c, one four bits higher 1024 + 16 c. bf16 has no such room, but taken as a bf16 by themselves
 // (subnormal, or of the lowest binade, which goes on in the same steps) the code is c 2^-133 and the one
-// four bits higher c 2^-129; a multiplication by 2^127 or 2^123 brings both to c / 64.
+// four bits higher c 2^-129; a multiplication by 2^127 or 2^123 brings both to c / 64. The sums are
+// multiplied by 64 at the end: exact, but for results below 2^-120, which were subnormal meanwhile.
+// (4-bit layer, 5 tokens: 71 us, with every code in the lowest bits 74 us.)
 template <bool F16>
 constexpr float kW4Unit = F16 ? 1.f : 64.f;
 template <bool F16>
