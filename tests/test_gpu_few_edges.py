@@ -1,0 +1,74 @@
+"""The few-token layer at the edges of fp32: SwiGLU where the gate closes.
+
+One token, x a unit vector and one expert (routing weight 1), so that gate and up are single weights,
+known exactly, and with one weight in each row of W_down an output is one element of h.
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+if not torch.cuda.is_available():  # pragma: no cover - collected on CPU, skipped there
+    pytestmark = pytest.mark.skip(reason="needs a CUDA device")
+
+import sparse_moe_expert_fp32_b200 as moe  # noqa: E402
+
+U = 2.0 ** -24
+BF16 = torch.bfloat16
+N = 64  # H and I
+
+
+def _layer(gate, up):
+    """Layer of one expert with gate[c] and up[c] in channel c, W_down the identity; the shared
+    expert's matrices are zero."""
+    s = moe.make_shape(1, N, 1, 1, N, N)
+    x = torch.zeros(1, N, dtype=BF16, device="cuda")
+    x[0, 0] = 1
+    w = {n: torch.zeros(*sh, dtype=BF16, device="cuda") for n, sh in
+         (("w_gate_up", (1, 2 * N, N)), ("w_down", (1, N, N)), ("ws_gate_up", (2 * N, N)), ("ws_down", (N, N)),
+          ("w_shared_gate", (N,)))}
+    w["w_router"] = torch.zeros(1, N, device="cuda")
+    w["w_gate_up"][0, :len(gate), 0] = torch.tensor(gate, dtype=torch.float64).to(BF16).cuda()
+    w["w_gate_up"][0, N:N + len(up), 0] = torch.tensor(up, dtype=torch.float64).to(BF16).cuda()
+    w["w_down"][0] = torch.eye(N, device="cuda").to(BF16)
+    return s, x, w
+
+
+def _run(s, x, w, group=0):
+    """(out [H], gate|up bank, down bank as the layer reads them, in 64 bits)."""
+    ws, out = moe.alloc_workspace(s), torch.full((1, N), 77.0, device="cuda")
+    if group:
+        q = moe.quantize_w4_experts(s, w, group)
+        moe.moe_layer_forward_few_w4(s, x, w, q, out, ws)
+        banks = []
+        for n in ("gate_up", "down"):
+            b = torch.empty_like(w["w_" + n], dtype=torch.float32)
+            moe.moe_dequantize_w4(q["q_" + n], q["s_" + n], b, group)
+            banks.append(b[0].double())
+    else:
+        moe.moe_layer_forward_few(s, x, w, out, ws)
+        banks = [w["w_gate_up"][0].double(), w["w_down"][0].double()]
+    assert moe.moe_device_status(ws)[0] == moe.MOE_OK
+    return out[0].double(), *banks
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [0, 32, 128])
+def test_closed_gates(group):
+    """h = SiLU(gate) up for gates whose exponential leaves fp32's range, and where gate times up does.
+
+    Tolerance: exp, the division and the four products of h and of its way to the output are within
+    24 u of h; below -87 exp(gate) is a subnormal, off by at most 4 steps of 2^-149 with the quotient's
+    rounding; below -104 it is 0, and h as small as that."""
+    pairs = [(-1.0, 1e30), (-60, 1e30), (-85, 1e35), (-87, 1e30), (-87.5, 1e30), (-88, 1e30), (-88.5, -1e33),
+             (-89, 1e35), (-89, 1e38), (-95, 1e37), (-100, 1e37), (-100, -3e38), (-103, 1e38), (-108, 1e38),
+             (-110, 3e38), (-1e4, 1e37), (-1e10, -1e30), (-1e20, 1e20), (-1e30, 1e30), (-1e37, 3e38),
+             (88.0, 3.0), (89, 1e30), (100, -1e30), (1e4, 1e30), (1e20, 1e10), (0.0, 1e30), (-50, 0.0)]
+    s, x, w = _layer(*zip(*pairs))
+    out, gu, dn = _run(s, x, w, group)
+    gate, up = gu[:N, 0], gu[N:, 0]
+    h = gate / (1 + torch.exp(-gate)) * up
+    want = dn @ h
+    small = torch.where(gate > -104, 4 * 2.0 ** -149 * (gate * up).abs(), h.abs())
+    tol = 24 * U * h.abs() + torch.where(gate < -87, small, 0.0)
+    err = (out - want).abs()
+    assert (err <= dn.abs() @ tol).all(), [(p, float(o), float(v)) for p, o, v in zip(pairs, out, want)]
