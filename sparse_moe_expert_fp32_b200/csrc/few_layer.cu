@@ -849,8 +849,9 @@ __device__ __forceinline__ void down_bf16(const FewArgs& a, FewShared& S, uint32
     for (int i = 0; i < NI; ++i) {
       float v0, v1;
       fold(sum[n][i], t4 < 2, v0, v1);
-      float v = v0 + (t4 & 1 ? 0.f : v1);  // third piece, or first and second
-      v += __shfl_xor_sync(0xffffffffu, v, 1);
+      // lane 0 has the first two pieces' sums, lane 1 the third's. An infinite weight gives the first
+      // its infinity or NaN, and the others NaN where h ends before them.
+      const float third = __shfl_xor_sync(0xffffffffu, v0, 1), v = fabsf(v0) <= FLT_MAX ? v0 + v1 + third : v0;
       if (t4 == 0) S.out[warp][8 * i + g][token] += open * v;
     }
   }

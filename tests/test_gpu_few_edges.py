@@ -1,4 +1,4 @@
-"""The few-token layer at the edges of fp32: SwiGLU where the gate closes.
+"""The few-token layer at the edges of fp32: SwiGLU where the gate closes, infinite weights.
 
 One token, x a unit vector and one expert (routing weight 1), so that gate and up are single weights,
 known exactly, and with one weight in each row of W_down an output is one element of h.
@@ -72,3 +72,20 @@ def test_closed_gates(group):
     tol = 24 * U * h.abs() + torch.where(gate < -87, small, 0.0)
     err = (out - want).abs()
     assert (err <= dn.abs() @ tol).all(), [(p, float(o), float(v)) for p, o, v in zip(pairs, out, want)]
+
+@pytest.mark.gpu
+def test_infinite_down_weights_times_short_h():
+    """An infinite weight times a finite h is an infinity, whichever of h's bits are zero, and NaN for
+    h = 0; other rows are as they were. (SiLU(128) is 128 in fp32: h has one significant bit.)"""
+    inf = float("inf")
+    s, x, w = _layer([128.0] * 16, [1.0, -1.0, 0.0] + [1.0] * 13)
+    w["w_down"][0, 20, 0], w["w_down"][0, 21, 1], w["w_down"][0, 22, 0] = inf, inf, -inf
+    w["w_down"][0, 23, 2] = inf                               # h = 0
+    w["w_down"][0, 24, 3], w["w_down"][0, 24, 4] = inf, -inf  # of either sign
+    w["w_down"][0, 25, 5] = float("nan")
+    w["ws_gate_up"][0, 0], w["ws_gate_up"][N, 0], w["ws_down"][26, 0] = 128, 1, inf  # the shared expert
+    out, gu, dn = _run(s, x, w)
+    want = dn @ (gu[:N, 0] * gu[N:, 0])
+    want[26] = inf
+    assert torch.equal(torch.nan_to_num(out, 7.0), torch.nan_to_num(want, 7.0))
+    assert torch.equal(out.isnan(), want.isnan()) and out.isnan().sum() == 3
