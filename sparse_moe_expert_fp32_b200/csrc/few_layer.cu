@@ -760,9 +760,13 @@ template <int FMT>
 __device__ void feed_h(Feeder& f, uint8_t* units) {
   const FewArgs& a = f.a;
   FewShared& S = f.S;
+  const int n1 = row_begin(a, blockIdx.x + 1);
+  // A CTA without output rows (H < grid) does not wait: its consumers leave without h, and the last one
+  // to leave sets the counter back to zero, which this thread, still looking, would wait for in vain.
+  // Where there are rows, the consumers leave after this thread has brought them h.
+  if (row_begin(a, blockIdx.x) == n1) return;
   grid_wait(a.sync + 1, S, a.status);
   asm volatile("fence.proxy.async;" ::: "memory");
-  const int n1 = row_begin(a, blockIdx.x + 1);
   Cursor done = f.cur;  // the oldest stage whose units are not known to be free
   int flight = 0, in_use = 0, at = 0;
   auto pop = [&] {

@@ -89,3 +89,36 @@ def test_infinite_down_weights_times_short_h():
     want[26] = inf
     assert torch.equal(torch.nan_to_num(out, 7.0), torch.nan_to_num(want, 7.0))
     assert torch.equal(out.isnan(), want.isnan()) and out.isnan().sum() == 3
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [0, 64])
+@pytest.mark.parametrize("H,T", [(64, 1), (64, 8), (128, 3)])
+def test_blocks_without_output_rows_do_not_wait_for_the_others(H, T, group):
+    """H is below the number of blocks: some have no output row and leave early. A block that still looked
+    at the grid's counters when the last one puts them back to zero would wait until its limit (seconds),
+    and the status would say so."""
+    g = torch.Generator(device="cuda").manual_seed(H + T)
+    s = moe.make_shape(T, H, 32, 4, 64, 64)
+    x = torch.randn(T, H, device="cuda", generator=g).to(BF16)
+    w = {n: (torch.randn(*sh, device="cuda", generator=g) * 0.05).to(BF16) for n, sh in
+         (("w_gate_up", (32, 128, H)), ("w_down", (32, H, 64)), ("ws_gate_up", (128, H)), ("ws_down", (H, 64)),
+          ("w_shared_gate", (H,)))}
+    w["w_router"] = torch.randn(32, H, device="cuda", generator=g) * 0.05
+    ws, out = moe.alloc_workspace(s), torch.empty(T, H, device="cuda")
+    if group:
+        q = moe.quantize_w4_experts(s, w, group)
+        call = lambda: moe.moe_layer_forward_few_w4(s, x, w, q, out, ws)  # noqa: E731
+    else:
+        call = lambda: moe.moe_layer_forward_few(s, x, w, out, ws)  # noqa: E731
+    call()
+    want = out.clone()
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    a.record()
+    for _ in range(3000):
+        call()
+    b.record()
+    b.synchronize()
+    assert torch.equal(out, want)
+    assert moe.moe_device_status(ws) == (moe.MOE_OK, 0)
+    assert a.elapsed_time(b) < 1500  # ms; a wait that runs out takes 2000 by itself
