@@ -408,7 +408,8 @@ moe_status moe_matvec_w4(int32_t T, int64_t N, int64_t K, int32_t group, moe_dty
 
 /*
  * The layer for a few tokens: moe_layer_forward in one kernel, for T <= 8 and T * H <= 65536
- * (MOE_ERR_UNSUPPORTED otherwise; moe_layer_forward takes any batch). Same arguments, workspace
+ * (MOE_ERR_UNSUPPORTED otherwise, and on a part of a device whose SMs are too few for the router
+ * of the shape; moe_layer_forward takes any batch). Same arguments, workspace
  * and errors as moe_layer_forward; the variant and the fp16 down operands are not used. It
  * differs in its arithmetic: the router's logits are summed in 64 bits (topk_ids are the exact
  * choice, equal logits -> lower index), h keeps its 24 bits, and nothing is added atomically,

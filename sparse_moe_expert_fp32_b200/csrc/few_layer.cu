@@ -57,6 +57,7 @@ constexpr int kFewBlock = kFewThreads + 2 * 32;  // and one warp that feeds them
 constexpr int kFewPairs = kFewMaxT * (kMaxK + 1);  // (token, expert) pairs, shared expert included
 constexpr int kFewRows = 32;                       // output rows of one pass of the down stage
 constexpr int kFewMaxStages = 16;
+constexpr int kFewParts = kFewWarps * kFewRows * kFewMaxT / 2;  // router partial sums; shares a place with sums of the tiles
 constexpr uint64_t kFewWaitNs = 2000000000ull;
 constexpr uint64_t kFewDrainNs = 200000000ull;
 constexpr int kBarConsumers = 1, kBarRouted = 2, kBarTeam = 3;  // named barriers
@@ -103,7 +104,7 @@ struct FewShared {
   int tag[kFewMaxStages];                   // number of the stage that a slot is filled with
   uint8_t stage_units[kFewMaxStages];       // units of h that a stage in flight uses
   union {
-    double part[2 * kFewWarps * 16 * kFewMaxT / 2];  // router partial sums: [stage][warp of the team][token]
+    double part[kFewParts];  // router partial sums: [stage][warp of the team][token]
     struct {
       uint64_t key[kFewMaxT][64];            // selection: candidates of a token
       uint16_t e[kFewMaxT][64];
@@ -1253,14 +1254,6 @@ few_layer_kernel(const __grid_constant__ FewArgs a, const __grid_constant__ FewM
   else feed<FMT>(a, m, S, ring, xs, xpitch);
 }
 
-}  // namespace
-
-bool few_supported(const moe_shape& s) {
-  return s.T <= kFewMaxT && (int64_t)s.T * s.H <= kFewMaxTH;
-}
-
-namespace {
-
 // Chunks of a row of K weights for stages of `stage` bytes with `rows` rows, at most `limit` blocks.
 FewChunks few_chunks(int K, int rows, bool w4, int shift, int stage, int limit) {
   FewChunks c;
@@ -1277,6 +1270,52 @@ FewChunks few_chunks(int K, int rows, bool w4, int shift, int stage, int limit) 
     c.sc = 0;
   }
   return c;
+}
+
+// The geometry of a call on `sms` SMs into `a` (shift: of the 4-bit experts, -1 for bf16); false if the kernel's
+// fixed capacities do not hold it. 148 SMs hold every shape within the stated limits; a part of a device may not.
+bool few_plan(const moe_shape& s, int shift, int sms, FewArgs& a) {
+  const bool w4 = shift >= 0;
+  a.shift = w4 ? shift : 0;
+  a.ldl = (s.E + 2) / 2 * 2;
+  a.T = s.T; a.H = s.H; a.E = s.E; a.k = s.k; a.I = s.I; a.Is = s.Is;
+  const int cap = kFewRows;
+  const int most_rows = (s.H + sms - 1) / sms, passes = (most_rows + cap - 1) / cap;
+  a.rows = (most_rows + passes - 1) / passes;
+  const int x_bytes = s.T * (2 * s.H + 64);
+  // Six stages of 24 KB; where x leaves less room, smaller ones, below 15 KB fewer of them: a stage costs
+  // its team some 700 clocks besides its weights. (8 tokens of H = 8192, I = 2048, 4-bit weights: six
+  // stages of 12 KB 484 us, four of 18 KB 433 us, three of 24 KB 450 us.)
+  const int most_bytes = 24576, least_bytes = 15360;
+  for (a.stages = 6;; --a.stages) {
+    for (a.stage_bytes = most_bytes;; a.stage_bytes -= 1024) {
+      a.gu_s = few_chunks(s.H, 16, false, 0, a.stage_bytes, 32);
+      a.gu = few_chunks(s.H, 16, w4, a.shift, a.stage_bytes, 32);
+      // the limit keeps a unit of h near 6 KB
+      a.dn_s = few_chunks(s.Is, a.rows, false, 0, a.stage_bytes, 32);
+      a.dn = few_chunks(s.I, a.rows, w4, a.shift, a.stage_bytes, w4 ? 8 : 32);
+      // 64 mod 128 bytes (banks), more of them than one stage can need
+      a.unit = std::max(a.dn_s.cb * 192, a.dn.cb * (w4 ? 768 : 192)) | 64;
+      a.h_bytes = (std::max(x_bytes, (s.T + 4) * a.unit) + 127) / 128 * 128;
+      if (kFewSharedBytes + a.h_bytes + (size_t)a.stages * a.stage_bytes <= kFewSmem) break;
+      if (a.stage_bytes <= least_bytes) break;
+    }
+    if (kFewSharedBytes + a.h_bytes + (size_t)a.stages * a.stage_bytes <= kFewSmem) break;
+    if (a.stages <= 3) return false;
+  }
+  // what is left holds more units of h: several groups of experts in flight
+  a.h_bytes = ((int)kFewSmem - (int)kFewSharedBytes - a.stages * a.stage_bytes) / 128 * 128;
+  a.units = std::min(a.h_bytes / a.unit, 64);
+  a.slot = (a.rows * 64 * a.dn.cb + 127) / 128 * 128 + (a.rows * a.dn.sc + 127) / 128 * 128;
+  // experts of a stage: 1, 2 or 4, so that each has as many of the team's warps; bf16: and so few that a
+  // warp's share of one is a chain of at most 8 instructions, as everywhere
+  const int fit = std::min(a.stage_bytes / a.slot, a.units / s.T);
+  a.group = a.dn.n > 1 || fit < 2 ? 1 : fit < kFewTeam ? 2 : kFewTeam;
+  while (!w4 && a.group * a.dn.cb > 8 * kFewTeam) a.group /= 2;
+  // the router's share of a CTA: a place for each partial sum, a thread for each logit
+  const int64_t rows = (s.E + 1 + sms - 1) / sms, chunks = (s.H + a.stage_bytes / 4 - 1) / (a.stage_bytes / 4);
+  return rows * chunks * kFewTeam * s.T <= kFewParts && rows * s.T <= kFewThreads &&
+         8 * s.T * a.ldl <= a.stages * a.stage_bytes;
 }
 
 bool few_map(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
@@ -1312,7 +1351,15 @@ bool few_scale_map(CUtensorMap* m, const void* base, uint64_t n, const FewChunks
   return few_map(m, base, 3, d3, s3, b3);
 }
 
+int few_shift(const moe_w4_experts* q) { return !q ? -1 : q->group == 32 ? 0 : q->group == 64 ? 1 : 2; }
+
 }  // namespace
+
+bool few_supported(const moe_shape& s, const moe_w4_experts* q, int sms) {
+  if (s.T > kFewMaxT || (int64_t)s.T * s.H > kFewMaxTH) return false;
+  FewArgs a{};
+  return s.T == 0 || few_plan(s, few_shift(q), sms, a);
+}
 
 cudaError_t launch_few_layer(const moe_shape& s, const Layout& L, char* ws, const uint16_t* x,
                              const moe_weights& w, const moe_w4_experts* q, float* out,
@@ -1322,7 +1369,6 @@ cudaError_t launch_few_layer(const moe_shape& s, const Layout& L, char* ws, cons
   a.w_router = w.w_router;
   a.bias = w.router_bias;
   a.wsg = static_cast<const uint16_t*>(w.w_shared_gate);
-  a.shift = q ? (q->group == 32 ? 0 : q->group == 64 ? 1 : 2) : 0;
   a.out = out;
   a.ids = ids;
   a.w = topk_w;
@@ -1330,45 +1376,10 @@ cudaError_t launch_few_layer(const moe_shape& s, const Layout& L, char* ws, cons
   a.logits = reinterpret_cast<double*>(ws + L.logits);
   a.h = reinterpret_cast<uint16_t*>(ws + L.few_h);
   a.ldh = L.ldh;
-  a.ldl = (s.E + 2) / 2 * 2;
   a.sync = reinterpret_cast<uint32_t*>(ws + L.status) + kFewSyncWord;
   a.status = reinterpret_cast<uint32_t*>(ws + L.status);
   a.per_tile = (uint32_t)(((1ull << 32) + s.I / 8 - 1) / (s.I / 8));
-  a.T = s.T; a.H = s.H; a.E = s.E; a.k = s.k; a.I = s.I; a.Is = s.Is;
-
-  const int cap = kFewRows;
-  const int most_rows = (s.H + sms - 1) / sms, passes = (most_rows + cap - 1) / cap;
-  a.rows = (most_rows + passes - 1) / passes;
-  const int x_bytes = s.T * (2 * s.H + 64);
-  // Six stages of 24 KB; where x leaves less room, smaller ones, below 15 KB fewer of them: a stage costs
-  // its team some 700 clocks besides its weights. (8 tokens of H = 8192, I = 2048, 4-bit weights: six
-  // stages of 12 KB 484 us, four of 18 KB 433 us, three of 24 KB 450 us.)
-  const int most_bytes = 24576, least_bytes = 15360;
-  for (a.stages = 6;; --a.stages) {
-    for (a.stage_bytes = most_bytes;; a.stage_bytes -= 1024) {
-      a.gu_s = few_chunks(s.H, 16, false, 0, a.stage_bytes, 32);
-      a.gu = few_chunks(s.H, 16, q != nullptr, a.shift, a.stage_bytes, 32);
-      // the limit keeps a unit of h near 6 KB
-      a.dn_s = few_chunks(s.Is, a.rows, false, 0, a.stage_bytes, 32);
-      a.dn = few_chunks(s.I, a.rows, q != nullptr, a.shift, a.stage_bytes, q ? 8 : 32);
-      // 64 mod 128 bytes (banks), more of them than one stage can need
-      a.unit = std::max(a.dn_s.cb * 192, a.dn.cb * (q ? 768 : 192)) | 64;
-      a.h_bytes = (std::max(x_bytes, (s.T + 4) * a.unit) + 127) / 128 * 128;
-      if (kFewSharedBytes + a.h_bytes + (size_t)a.stages * a.stage_bytes <= kFewSmem) break;
-      if (a.stage_bytes <= least_bytes) break;
-    }
-    if (kFewSharedBytes + a.h_bytes + (size_t)a.stages * a.stage_bytes <= kFewSmem) break;
-    if (a.stages <= 3) return cudaErrorInvalidValue;
-  }
-  // what is left holds more units of h: several groups of experts in flight
-  a.h_bytes = ((int)kFewSmem - (int)kFewSharedBytes - a.stages * a.stage_bytes) / 128 * 128;
-  a.units = std::min(a.h_bytes / a.unit, 64);
-  a.slot = (a.rows * 64 * a.dn.cb + 127) / 128 * 128 + (a.rows * a.dn.sc + 127) / 128 * 128;
-  // experts of a stage: 1, 2 or 4, so that each has as many of the team's warps; bf16: and so few that a
-  // warp's share of one is a chain of at most 8 instructions, as everywhere
-  const int fit = std::min(a.stage_bytes / a.slot, a.units / s.T);
-  a.group = a.dn.n > 1 || fit < 2 ? 1 : fit < kFewTeam ? 2 : kFewTeam;
-  while (!q && a.group * a.dn.cb > 8 * kFewTeam) a.group /= 2;
+  if (!few_plan(s, few_shift(q), sms, a)) return cudaErrorInvalidValue;
 
   FewMaps m;
   bool ok = few_weight_map(&m.gu_s, w.ws_gate_up, s.Is, a.gu_s, 2 * (uint64_t)s.H, 2, 1, 8) &&
@@ -1384,7 +1395,7 @@ cudaError_t launch_few_layer(const moe_shape& s, const Layout& L, char* ws, cons
     ok = ok && few_weight_map(&m.gu, w.w_gate_up, s.I, a.gu, 2 * (uint64_t)s.H, 2, s.E, 8) &&
          few_weight_map(&m.dn, w.w_down, s.H, a.dn, 2 * (uint64_t)s.I, 1, s.E, a.rows);
   }
-  if (!ok || 8 * s.T * a.ldl > a.stages * a.stage_bytes) return cudaErrorInvalidValue;
+  if (!ok) return cudaErrorInvalidValue;
 
   const size_t smem = kFewSharedBytes + a.h_bytes + (size_t)a.stages * a.stage_bytes;
   const void* fn = !q ? (const void*)few_layer_kernel<-1>

@@ -564,12 +564,12 @@ moe_status moe_layer_forward_few(const moe_shape* shape, const void* x, const mo
   MOE_TRY(check_router_weights(weights));
   MOE_TRY(check_expert_weights(weights));
   MOE_TRY(check_layer_io(x, out, topk_ids, topk_w, gap));
-  if (!few_supported(s)) return MOE_ERR_UNSUPPORTED;
+  const int sms = sm_count_host();
+  if (!few_supported(s, nullptr, sms)) return MOE_ERR_UNSUPPORTED;
   MOE_TRY(check_ws(s, ws, ws_bytes));
   if (s.T == 0) return MOE_OK;
   MOE_CUDA(launch_few_layer(s, layout(s), static_cast<char*>(ws), static_cast<const uint16_t*>(x),
-                            *weights, nullptr, out, topk_ids, topk_w, gap, sm_count_host(),
-                            (cudaStream_t)stream));
+                            *weights, nullptr, out, topk_ids, topk_w, gap, sms, (cudaStream_t)stream));
   return MOE_OK;
 }
 
@@ -586,12 +586,12 @@ moe_status moe_layer_forward_few_w4(const moe_shape* shape, const void* x,
       w4_shift(experts->group) < 0)
     return MOE_ERR_INVALID_ARG;
   MOE_TRY(check_layer_io(x, out, topk_ids, topk_w, gap));
-  if (!few_supported(s)) return MOE_ERR_UNSUPPORTED;
+  const int sms = sm_count_host();
+  if (!few_supported(s, experts, sms)) return MOE_ERR_UNSUPPORTED;
   MOE_TRY(check_ws(s, ws, ws_bytes));
   if (s.T == 0) return MOE_OK;
   MOE_CUDA(launch_few_layer(s, layout(s), static_cast<char*>(ws), static_cast<const uint16_t*>(x),
-                            *weights, experts, out, topk_ids, topk_w, gap, sm_count_host(),
-                            (cudaStream_t)stream));
+                            *weights, experts, out, topk_ids, topk_w, gap, sms, (cudaStream_t)stream));
   return MOE_OK;
 }
 

@@ -197,7 +197,7 @@ cudaError_t launch_matvec_w4(int T, int64_t N, int64_t K, int shift, const uint1
                              int64_t ldx, const uint8_t* q, const uint16_t* s, void* y, bool y_f32,
                              int64_t ldy, int sms, cudaStream_t st);
 // The layer for a few tokens in one kernel (few_layer.cu); q = NULL: bf16 experts.
-bool few_supported(const moe_shape& s);
+bool few_supported(const moe_shape& s, const moe_w4_experts* q, int sms);
 cudaError_t launch_few_layer(const moe_shape& s, const Layout& L, char* ws, const uint16_t* x,
                              const moe_weights& w, const moe_w4_experts* q, float* out,
                              int32_t* ids, float* topk_w, float* gap, int sms, cudaStream_t st);
