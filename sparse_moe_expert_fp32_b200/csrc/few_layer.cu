@@ -125,6 +125,7 @@ struct FewShared {
   uint8_t act_mask[kFewMaxT * kMaxK + 1];
   int n_act;
   int aborted;
+  int parked;  // feeders that arrive on no barrier: not before the experts are known, or never again
 };
 
 
@@ -138,19 +139,32 @@ __device__ __forceinline__ void give_up(FewShared& S, uint32_t* status) {
   set_flag(status, kFlagTimeout);
 }
 
+// What a thread does whose wait has run out, or that of another thread of the block. A consumer goes on
+// without its stage and gives back a slot whose copies may still be in flight. Nobody may arrive on the
+// slot's barrier until they have landed, so it waits (with a limit) until the feeders have stopped: they do
+// at their next wait, at the end of the grid's barrier, or where they wait for the experts. x and the logits
+// have no feeder that waits for them to land. (Kept out of the loops: a test of each wait's result there
+// cost 1 token 0.5 to 0.8 us, this 0.3 to 0.5.)
+__device__ __noinline__ bool run_out(uint64_t* bar, uint32_t parity, FewShared& S) {
+  if (threadIdx.x >= kFewThreads) return false;
+  __threadfence_block();
+  const uint64_t t0 = globaltimer_ns();
+  while (*reinterpret_cast<volatile int*>(&S.parked) != 2 && globaltimer_ns() - t0 < 2 * kFewWaitNs) {
+  }
+  if (bar == &S.x_full || bar == &S.logits_full) drain_phase(bar, parity);
+  return false;
+}
+
 // Bounded wait on an mbarrier phase; false once any wait of the block has run out.
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, FewShared& S, uint32_t* status) {
   uint64_t t0 = 0;
   for (uint32_t spin = 1;; ++spin) {
     if (ptx::mbar_try_wait(bar, parity)) return true;
     if ((spin & 31u) == 0) {  // reading the clock is slow: only in long waits
-      if (*reinterpret_cast<volatile int*>(&S.aborted)) return false;
+      if (*reinterpret_cast<volatile int*>(&S.aborted)) return run_out(bar, parity, S);
       const uint64_t t = globaltimer_ns();
       if (!t0) t0 = t;
-      if (t - t0 > kFewWaitNs) {
-        give_up(S, status);
-        return false;
-      }
+      if (t - t0 > kFewWaitNs) give_up(S, status);
     }
   }
 }
@@ -227,13 +241,13 @@ __device__ __noinline__ void tag_slow(volatile int* tag, int i, FewShared& S, ui
   uint64_t t0 = 0;
   for (uint32_t spin = 1; *tag != i; ++spin)
     if ((spin & 255u) == 0) {
-      if (*reinterpret_cast<volatile int*>(&S.aborted)) return;
-      const uint64_t t = globaltimer_ns();
-      if (!t0) t0 = t;
-      if (t - t0 > kFewWaitNs) {
-        give_up(S, status);
+      if (*reinterpret_cast<volatile int*>(&S.aborted)) {
+        run_out(nullptr, 0u, S);
         return;
       }
+      const uint64_t t = globaltimer_ns();
+      if (!t0) t0 = t;
+      if (t - t0 > kFewWaitNs) give_up(S, status);
     }
 }
 __device__ __forceinline__ void wait_stage(const Place& at, FewShared& S, uint32_t* status) {
@@ -765,7 +779,7 @@ __device__ void feed_h(Feeder& f, uint8_t* units) {
   // A CTA without output rows (H < grid) does not wait: its consumers leave without h, and the last one
   // to leave sets the counter back to zero, which this thread, still looking, would wait for in vain.
   // Where there are rows, the consumers leave after this thread has brought them h.
-  if (row_begin(a, blockIdx.x) == n1) return;
+  if (row_begin(a, blockIdx.x) == n1 || !f.ok) return;
   grid_wait(a.sync + 1, S, a.status);
   asm volatile("fence.proxy.async;" ::: "memory");
   Cursor done = f.cur;  // the oldest stage whose units are not known to be free
@@ -1220,13 +1234,19 @@ __device__ void feed(const FewArgs& a, const FewMaps& m, FewShared& S, uint8_t* 
   if (lane == 0) {
     feed_router(f, xs, xpitch, h);
     feed_gate_up<FMT>(f, m, h, tile, ns);
+    atomicAdd(&S.parked, 1);
   }
   __syncwarp();
   ptx::bar_sync(kBarRouted, kFewBlock);
   if (lane != 0) return;
+  // a consumer that has run out and seen this feeder parked is seen here
+  atomicSub(&S.parked, 1);
+  __threadfence_block();
+  if (*reinterpret_cast<volatile int*>(&S.aborted)) f.ok = false;
   feed_gate_up<FMT>(f, m, h, tile, ns + (S.n_act - 1) * (a.I / 8));
   if (h) feed_h<FMT>(f, xs);
   else feed_down<FMT>(f, m);
+  atomicAdd(&S.parked, 1);
   f.drain();
 }
 
@@ -1246,7 +1266,7 @@ few_layer_kernel(const __grid_constant__ FewArgs a, const __grid_constant__ FewM
     ptx::mbar_init(&S.x_full, 1);
     ptx::mbar_init(&S.logits_full, 1);
     for (int i = 0; i < a.stages; ++i) S.tag[i] = -1;
-    S.aborted = 0;
+    S.aborted = S.parked = 0;
     ptx::fence_mbar_init();
   }
   __syncthreads();

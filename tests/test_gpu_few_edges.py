@@ -122,3 +122,43 @@ def test_blocks_without_output_rows_do_not_wait_for_the_others(H, T, group):
     assert torch.equal(out, want)
     assert moe.moe_device_status(ws) == (moe.MOE_OK, 0)
     assert a.elapsed_time(b) < 1500  # ms; a wait that runs out takes 2000 by itself
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("group", [0, 32])
+def test_a_barrier_that_runs_out_is_reported_and_leaves_the_workspace_ready(group):
+    """The counter of the first grid barrier (the workspace's 17th word) starts one below zero, so that it
+    never gets to the number of blocks (a block adds one to it before it looks). Every block's wait ends at
+    its limit, the status says so, and the next call on the same workspace is right."""
+    T, H, E, k, I = 3, 256, 16, 4, 128
+    g = torch.Generator(device="cuda").manual_seed(1)
+    s = moe.make_shape(T, H, E, k, I, I)
+    x = torch.randn(T, H, device="cuda", generator=g).to(BF16)
+    w = {n: (torch.randn(*sh, device="cuda", generator=g) * 0.05).to(BF16) for n, sh in
+         (("w_gate_up", (E, 2 * I, H)), ("w_down", (E, H, I)), ("ws_gate_up", (2 * I, H)), ("ws_down", (H, I)),
+          ("w_shared_gate", (H,)))}
+    w["w_router"] = torch.randn(E, H, device="cuda", generator=g) * 0.05
+    ws = moe.alloc_workspace(s)
+    raw = torch.full((T * H + 2048,), 7.0, device="cuda")
+    out = raw[1024:1024 + T * H].view(T, H)
+    ids = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+    q = moe.quantize_w4_experts(s, w, group) if group else None
+
+    def call():
+        if group:
+            moe.moe_layer_forward_few_w4(s, x, w, q, out, ws, topk_ids=ids)
+        else:
+            moe.moe_layer_forward_few(s, x, w, out, ws, topk_ids=ids)
+
+    call()
+    want = out.clone(), ids.clone()
+    ws.view(torch.int32)[16] = -1
+    call()
+    status, flags = moe.moe_device_status(ws)
+    assert status == moe.MOE_ERR_DEVICE_TIMEOUT and flags == 2
+    assert ((ids >= 0) & (ids < E)).all()
+    assert (raw[:1024] == 7).all() and (raw[1024 + T * H:] == 7).all()
+    for _ in range(3):
+        call()
+        assert torch.equal(out, want[0]) and torch.equal(ids, want[1])
+    assert moe.moe_device_status(ws) == (moe.MOE_OK, 0)
