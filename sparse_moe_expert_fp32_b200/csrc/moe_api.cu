@@ -563,11 +563,11 @@ moe_status moe_layer_forward_few(const moe_shape* shape, const void* x, const mo
   const moe_shape& s = *shape;
   MOE_TRY(check_router_weights(weights));
   MOE_TRY(check_expert_weights(weights));
-  MOE_TRY(check_layer_io(x, out, topk_ids, topk_w, gap));
   const int sms = sm_count_host();
   if (!few_supported(s, nullptr, sms)) return MOE_ERR_UNSUPPORTED;
   MOE_TRY(check_ws(s, ws, ws_bytes));
-  if (s.T == 0) return MOE_OK;
+  if (s.T == 0) return MOE_OK;  // before the tokens' pointers: an empty tensor has none
+  MOE_TRY(check_layer_io(x, out, topk_ids, topk_w, gap));
   MOE_CUDA(launch_few_layer(s, layout(s), static_cast<char*>(ws), static_cast<const uint16_t*>(x),
                             *weights, nullptr, out, topk_ids, topk_w, gap, sms, (cudaStream_t)stream));
   return MOE_OK;
@@ -585,11 +585,11 @@ moe_status moe_layer_forward_few_w4(const moe_shape* shape, const void* x,
       !aligned16(experts->q_down) || !aligned16(experts->s_down) ||
       w4_shift(experts->group) < 0)
     return MOE_ERR_INVALID_ARG;
-  MOE_TRY(check_layer_io(x, out, topk_ids, topk_w, gap));
   const int sms = sm_count_host();
   if (!few_supported(s, experts, sms)) return MOE_ERR_UNSUPPORTED;
   MOE_TRY(check_ws(s, ws, ws_bytes));
-  if (s.T == 0) return MOE_OK;
+  if (s.T == 0) return MOE_OK;  // before the tokens' pointers: an empty tensor has none
+  MOE_TRY(check_layer_io(x, out, topk_ids, topk_w, gap));
   MOE_CUDA(launch_few_layer(s, layout(s), static_cast<char*>(ws), static_cast<const uint16_t*>(x),
                             *weights, experts, out, topk_ids, topk_w, gap, sms, (cudaStream_t)stream));
   return MOE_OK;

@@ -46,3 +46,19 @@ def test_limits_do_not_depend_on_the_device(group):
 ])
 def test_a_part_of_a_device_that_cannot_hold_the_router_is_refused(shape, sms, ok, group):
     assert _fits(shape, group, sms) == ok
+
+
+@pytest.mark.parametrize("group", [0, 32])
+def test_no_tokens_need_no_addresses_of_theirs(group):
+    """T == 0 is valid; a framework's tensor without elements has a null address."""
+    L, A = moe.lib(), 4096
+    s, w = moe.make_shape(0, 128, 8, 2, 64, 64), moe.moe_weights(A, 0, A, A, A, A, A)
+    before = moe.moe_launch_count()
+    head = (ctypes.byref(s), None, ctypes.byref(w))
+    tail = (None, None, None, None, A, moe.moe_workspace_bytes(s), None)
+    if group:
+        q = moe.moe_w4_experts(A, A, A, A, group)
+        assert L.moe_layer_forward_few_w4(*head, ctypes.byref(q), *tail) == moe.MOE_OK
+    else:
+        assert L.moe_layer_forward_few(*head, *tail) == moe.MOE_OK
+    assert moe.moe_launch_count() == before
