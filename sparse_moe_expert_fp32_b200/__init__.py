@@ -612,21 +612,38 @@ def prepare_down_f16(shape: moe_shape, weights: dict, stream=None) -> dict:
     return out
 
 
+def _allocating_on(stream, device):
+    """A context whose allocations belong to `stream`: what the current stream's allocator gives out may
+    still be read by work that is enqueued there."""
+    import contextlib
+
+    import torch
+
+    if stream is None or device.type != "cuda":
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream, device=device) if stream
+                  else torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
+
+
 def quantize_w4(w, group: int = 32, stream=None):
-    """A bf16 matrix or bank [..., K] in 4-bit groups: (codes uint8, scales bf16), allocated."""
+    """A bf16 matrix or bank [..., K] in 4-bit groups: (codes uint8, scales bf16), allocated and
+    written on `stream` (where w has to be there)."""
     import torch
 
     lead = tuple(w.shape[:-1])
-    q = torch.empty(lead + (moe_w4_row_bytes(w.shape[-1]),), dtype=torch.uint8, device=w.device)
-    s = torch.empty(lead + (moe_w4_row_scales(w.shape[-1], group),), dtype=torch.bfloat16,
-                    device=w.device)
+    with _allocating_on(stream, w.device):
+        q = torch.empty(lead + (moe_w4_row_bytes(w.shape[-1]),), dtype=torch.uint8, device=w.device)
+        s = torch.empty(lead + (moe_w4_row_scales(w.shape[-1], group),), dtype=torch.bfloat16,
+                        device=w.device)
     moe_quantize_w4(w, q, s, group, stream)
     return q, s
 
 
 def quantize_w4_experts(shape: moe_shape, weights: dict, group: int = 32, stream=None) -> dict:
     """The 4-bit expert pre-pass on a weight dict (run once): allocates and returns {q_gate_up,
-    s_gate_up, q_down, s_down, group} on the routed banks' device."""
+    s_gate_up, q_down, s_down, group} on the routed banks' device, made on `stream`."""
     E, H, I = shape.E, shape.H, shape.I
     gu, dn = weights["w_gate_up"].view(E, 2 * I, H), weights["w_down"].view(E, H, I)
     q = {"group": int(group)}
