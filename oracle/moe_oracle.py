@@ -426,11 +426,13 @@ def combine(y: np.ndarray, y_shared: np.ndarray, assign_row: np.ndarray, weights
     return out
 
 
-def forward_inputs(inp, rows=None, forced_ids=None, fp8: Optional[Fp8Experts] = None) -> dict:
+def forward_inputs(inp, rows=None, forced_ids=None, fp8: Optional[Fp8Experts] = None,
+                   w4: Optional[W4Experts] = None) -> dict:
     """moe_forward on a ``synth.HostInputs``; ``rows`` selects a token subset. With ``fp8``
-    the routed experts are that FP8 bank (dequantised); the rest of the layer is unchanged."""
+    or ``w4`` the routed experts are that bank (dequantised); the rest of the layer is unchanged."""
     x = inp.x if rows is None else inp.x[np.asarray(rows)]
-    gu, dn = (fp8.gate_up, fp8.down) if fp8 is not None else (inp.gate_up, inp.down)
+    bank = fp8 or w4 or inp
+    gu, dn = bank.gate_up, bank.down
     return moe_forward(x, inp.w_router, inp.router_bias, gu, dn,
                        inp.ws_gate_up, inp.ws_down, inp.w_shared_gate, inp.cfg.k,
                        forced_ids=forced_ids)
