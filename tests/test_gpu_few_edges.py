@@ -74,6 +74,25 @@ def test_closed_gates(group):
     assert (err <= dn.abs() @ tol).all(), [(p, float(o), float(v)) for p, o, v in zip(pairs, out, want)]
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+def test_h_keeps_24_bits(group):
+    """h goes to the down product in three pieces of 8 bits. Its way there and to the output is within
+    24 u (exp 4, division 4, the sum and the products 1 each, the pieces' sum and, for 4-bit weights,
+    their scales 5); without the third piece it would be up to 512 u off."""
+    g = torch.Generator().manual_seed(3)
+    gate, up = torch.randn(N, generator=g) * 2, torch.randn(N, generator=g)
+    s, x, w = _layer(gate.tolist(), up.tolist())
+    out, gu, dn = _run(s, x, w, group)
+    gate, up = gu[:N, 0], gu[N:, 0]
+    h = gate / (1 + torch.exp(-gate)) * up
+    step = torch.exp2(torch.floor(torch.log2(h.abs())) - 15)  # two pieces: 16 bits
+    short = torch.trunc(h / step) * step
+    tol = 24 * U * (dn @ h).abs()
+    assert ((out - dn @ h).abs() <= tol).all()
+    assert ((dn @ (short - h)).abs() > 2 * tol).sum() > N // 2  # what this test is to see
+
+
+@pytest.mark.gpu
 def test_infinite_down_weights_times_short_h():
     """An infinite weight times a finite h is an infinity, whichever of h's bits are zero, and NaN for
     h = 0; other rows are as they were. (SiLU(128) is 128 in fp32: h has one significant bit.)"""
