@@ -389,7 +389,8 @@ moe_status moe_layer_forward_fp8(const moe_shape* shape, const void* x,
  *   format above; x is MOE_BF16 or MOE_F16 with row stride ldx elements, y is MOE_F32 or x's
  *   type with row stride ldy (elements between and behind rows are left as they are). x and y
  *   need only their element's alignment. Weights enter exactly, sums are fp32, and y is rounded
- *   once. T == 0, N == 0 and rows == 0 are valid and enqueue nothing.
+ *   once. A group is summed before its scale: below 2^124 |x| cannot take that sum out of fp32.
+ *   T == 0, N == 0 and rows == 0 are valid and enqueue nothing.
  * All asynchronous on `stream`, no workspace. Errors: MOE_ERR_INVALID_ARG (a negative size,
  * another group or type, a stride below its row, a null or misaligned pointer),
  * MOE_ERR_UNSUPPORTED (T > 16, K > 2^20, more than 2^31 rows), MOE_ERR_CUDA.
@@ -411,8 +412,9 @@ moe_status moe_matvec_w4(int32_t T, int64_t N, int64_t K, int32_t group, moe_dty
  * (MOE_ERR_UNSUPPORTED otherwise, and on a part of a device whose SMs are too few for the router
  * of the shape; moe_layer_forward takes any batch). Same arguments, workspace
  * and errors as moe_layer_forward; the variant and the fp16 down operands are not used. It
- * differs in its arithmetic: the router's logits are summed in 64 bits (topk_ids are the exact
- * choice, equal logits -> lower index), h keeps its 24 bits, and nothing is added atomically,
+ * differs in its arithmetic: the router's logits are summed and compared in 64 bits (equal ones ->
+ * lower index; logits that only rounding to fp32 makes equal are a tie in moe_layer_forward and
+ * none here), h keeps its 24 bits, and nothing is added atomically,
  * so equal calls give equal bits. A token's output depends on its own experts alone.
  * The kernel's blocks wait for one another (a cooperative launch), each wait bounded: if one ran
  * out, moe_device_status reports MOE_ERR_DEVICE_TIMEOUT and the outputs are unspecified. The

@@ -5,9 +5,9 @@
 // With a few tokens the layer is the reading of the activated experts' weights; launches, and
 // the waits between them, are the rest. So one cooperative kernel, one CTA per SM, runs the
 // stages with two grid-wide barriers between them:
-//   1. logits. A CTA takes E / grid rows of the router matrix; sums in 64 bits, so that the
-//      choice of experts is the exact one (a near-tie decided by rounding would change the
-//      output by whole experts).
+//   1. logits. A CTA takes E / grid rows of the router matrix; sums and comparisons in 64 bits
+//      (a near-tie decided by fp32 rounding would change the output by whole experts). The calls
+//      for whole batches compare logits rounded to fp32: what is a tie there is none here.
 //   2. shared expert's gate|up tiles, which need no routing, while the barrier fills.
 //   -- barrier: all logits are there. Every CTA selects the top-k of all tokens for itself.
 //   3. gate|up tiles of the chosen experts: 8 channels (8 gate rows and the 8 up rows) by the full
@@ -30,12 +30,14 @@
 //
 // Measured on one B200, weights not in L2, H = 2560, E = 512, k = 10, I = Is = 640 unless said; the
 // floor is the weights' bytes at the measured copy rate of 6.56 TB/s:
-//   bf16   1 token 35 us (floor 17), 8 tokens 146 us (115: 5.1 TB/s)
+//   bf16   1 token 35.3 us (floor 17), 8 tokens 146 us (115: 5.1 TB/s)
 //          4 tokens, H = 8192, E = 64, I = Is = 2048, some 26 experts chosen: 446 us (415: 6.1 TB/s)
 //   4-bit  1 token 29 us (6.5), 5 tokens 66 us (21); 8 tokens, H = 8192, I = 2048: 439 us (204)
-// bf16 is bound by HBM with about 10 us before the first expert's weights can be asked for (the router,
-// a barrier, the choice) and 4 us at the second barrier; 4-bit weights by the instructions that unpack
-// them (some 28 for each MMA, 1.6 of 4 a clock and SM), which take twice the time of their bytes.
+// bf16 with several tokens is bound by HBM. One token: a layer with 1 MB of weights takes 16.4 us, which is
+// launch, router, two grid barriers and the choice, none of them hidden. 4-bit weights are at no limit
+// of the hardware: a clock and SM executes 1.55 of 4 instructions, 26 for each MMA, at 21 % of the DRAM rate.
+// 9 of the 26 unpack codes; the rest of a block's work, and what surrounds the 5 blocks that a warp has
+// of a tile (wait, fold, barrier, epilogue), are dependent chains, and three warps a scheduler cover little.
 #include <float.h>
 
 #include <algorithm>

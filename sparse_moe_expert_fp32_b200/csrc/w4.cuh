@@ -119,7 +119,8 @@ __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c
 
 // One word of codes -> the four pairs (2 m, 2 m + 1), m = 0..3, of (c - 8) / kW4Unit: exact, and
 // without moving every code to the lowest bits. fp16: a code in the low mantissa bits of 1024 is
-// 1024 + c, one four bits higher 1024 + 16 c. bf16 has no such room, but taken as a bf16 by themselves
+// 1024 + c, one four bits higher 1024 + 16 c (the method of Kim, Henry, Fahim and Hassan Awadalla, "Who
+// Says Elephants Can't Run", 2022). bf16 has no such room, but taken as a bf16 by themselves
 // (subnormal, or of the lowest binade, which goes on in the same steps) the code is c 2^-133 and the one
 // four bits higher c 2^-129; a multiplication by 2^127 or 2^123 brings both to c / 64. The sums are
 // multiplied by 64 at the end: exact, but for results below 2^-120, which were subnormal meanwhile.

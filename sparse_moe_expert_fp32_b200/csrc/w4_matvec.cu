@@ -2,18 +2,21 @@
 //
 //   y[t, n] = sum_k x[t, k] (c[n, k] - 8) s[n, k / group]
 //
-// Bound by the weight bytes, 1/2 + 2/group each, and close to it by the arithmetic that makes
-// MMA operands of them. A group of warps takes 32 matrix rows (16 if there are few) and splits
-// their 128-element blocks; the fewer rows there are, the more warps a group has, so that small
-// matrices still spread over all SMs without a second launch. The codes come two blocks ahead; x is
+// A group of warps takes 32 matrix rows (16 if there are few) and splits
+// their 128-element blocks; the fewer rows there are, the more warps a group has, without a second
+// launch. 16 warps in whole groups make a CTA, so 75 to 148 of 148 SMs have one unless the matrix is
+// large (5000 rows of 2560: 79; 65536 rows: 128). The codes come two blocks ahead; x is
 // staged in shared memory. The MMA's A is 16
 // matrix rows, made in registers, its columns are 8 rows of x. The codes enter as exact
 // integers; the fp32 sum over a scale group is multiplied by the scale and added to the running
 // fp32 sums, so no product or weight is rounded.
 //
 // Measured on one B200, weights not in L2 (floor: their bytes at 6.56 TB/s): 1 row by 65536 x 8192,
-// groups of 128, 73 us (42); 16 rows 107 us; 5 rows by 4099 x 2501 7 us on the device. 16 rows do
-// twice the MMAs and fma of 8 for the same weights. A ring of three blocks a warp took 1 row from 85
+// groups of 128, 73 us (42); 16 rows 107 us; 5 rows by 4099 x 2501 7 us on the device. Neither HBM nor
+// the instructions are at their limit: 1 row 48 % of the DRAM rate and 2.4 of 4 instructions a clock (on the
+// SMs that have a CTA; 19 for each MMA), 16 rows 31 % and 2.0 (12); four warps a scheduler, each with 64
+// bytes of a row to a request, wait for the copies, for the pipe that unpacks, and for one another. 16 rows
+// in groups of 32 or 64 spill some 40 bytes. A ring of three blocks a warp took 1 row from 85
 // to 73 us against one block ahead in registers; it leaves x 128 KB, since x in twice as many chunks
 // costs 16 rows 8 us.
 #include <cuda_fp16.h>
@@ -241,8 +244,8 @@ cudaError_t launch_matvec_w4(int T, int64_t N, int64_t K, int shift, const uint1
   const int64_t most = kMvXBytes / (2 * T) / kW4Block * kW4Block;
   a.kc = (int)std::min(w4_blocks(K) * kW4Block, most);
   // 32 rows a group, 16 where that leaves SMs without one (32: 1 row by 65536 x 8192 73 us, 16: 84 us);
-  // and so many warps a group that the
-  // groups fill the device's warps once, at most one warp for a block
+  // and so many warps a group (a power of two) that the
+  // groups fill the device's warps once, fewer than two for a block
   const int np = N > (int64_t)sms * 32 ? 2 : 1;
   a.groups = (N + 16 * np - 1) / (16 * np);
   const int nb = (int)w4_blocks(a.kc);

@@ -5,11 +5,13 @@
 // Half a warp takes one storage block of 128 elements: lane 4 j + t reads elements
 // 32 j + 8 t .. + 7 (16 bytes, in row order) and writes word 4 t + j, so a block is one
 // 256-byte read and one 64-byte write, and a group's maximum is a shuffle over 4, 8 or 16
-// lanes. Four blocks a half warp are in flight. Bound by HBM: 2 bytes read and 1/2 + 2/group
+// lanes. Four blocks a half warp are in flight. 2 bytes read and 1/2 + 2/group
 // written per weight. 40960 x 2560 in groups of 32: 65 us, 131072 x 2048 in groups of 128: 155 us
 // (4.3 TB/s; the copy rate is 6.56), and back to fp32 104 us (4.6 TB/s), to bf16 114 us (5.9 TB/s).
-// Per eight weights a lane has some 60 instructions, which is what holds the way there back. 32 CTAs
-// an SM in turn are 5 to 15 % faster than the 8 that fit at once: no tail of slow ones.
+// The way there is held back by its instructions: 126 (groups of 128) for a lane's eight weights, 2.96 of 4
+// a clock, at 48 % of the DRAM rate. Back to fp32 by its stores: a lane writes its 32 bytes as two halves, so a
+// store instruction covers half of each sector it touches (32 sectors where 16 hold the data); to bf16 by HBM.
+// 32 CTAs an SM in turn are 5 to 15 % faster than the 8 that fit at once: no tail of slow ones.
 //
 // The quotient without a division: with 8-bit significands w / scale is either exactly half
 // way between two integers or at least 2^-10 away from it (for |w / scale| >= 1/4 its
