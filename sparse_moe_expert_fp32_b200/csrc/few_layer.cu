@@ -707,7 +707,7 @@ __device__ __forceinline__ void gate_up_tiles(const FewArgs& a, FewShared& S, ui
             }
           const int pair = routed ? S.act_pair[s] + __popc(m & ((1u << t) - 1u)) : t;
           // SiLU first, and from exp(-|gate|) <= 1: a quotient of numbers that fp32 holds, whatever the
-          // gate, and no product that h itself does not reach
+          // gate, and no product beyond what SiLU(gate) up itself reaches
           const float e = expf(-fabsf(gate)), silu = gate * __fdividef(gate < 0.f ? e : 1.f, 1.f + e);
           const float h = silu * up * (routed ? S.pair_w[pair] : 1.f);
           // three truncated pieces: 8 + 8 + 8 significant bits, h exactly (an infinity or NaN in
